@@ -353,6 +353,198 @@ PDA_API int32_t pda_plan_kernel(const pda_params* params);
 PDA_API pda_status pda_hbm_read_probe(const void* buf, size_t bytes, uint64_t* sink,
                                       pda_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Latent caches. A latent cache holds, for every token, one latent vector c
+ * (latent_dim elements) and one rotated key part r (rope_dim elements) that
+ * all query heads share. Two ways of attending to it:
+ *
+ *  - absorbed (paged_latent_decode): the key up-projection is folded into the
+ *    query, so key j is [c_j | r_j] and value j is c_j for every head; the
+ *    value up-projection is applied to the output by the caller. For one or a
+ *    few query rows per sequence: each cached row is read once for all heads.
+ *  - expanded (latent_prefill_attn): the caller multiplies the latents out to
+ *    keys and values per head; r_j stays shared. For many query rows.
+ *
+ * Rows enter the pages with paged_latent_append and come back, as bf16, with
+ * paged_latent_gather (a cached prefix that is to be expanded).
+ *
+ * Pools: latent_pages [num_pages, page_size, latent_dim] and rope_pages
+ * [num_pages, page_size, rope_dim], page tables as for paged_decode_attn.
+ *  - PDA_KV_BF16: both pools bf16.
+ *  - PDA_KV_FP8_E4M3: latent_pages uint8 e4m3 codes with one power-of-two
+ *    scale per row, latent_scales uint8 [num_pages, page_size]: value = code *
+ *    2^(scale - 127). rope_pages stays bf16 (rotated keys carry positions and
+ *    lose more than the latents do). The exponent scale - 127 lies in [-30, 30];
+ *    bytes outside are read as the nearer end. A power of two costs nothing
+ *    against a free scale (e4m3 is a floating format) and makes code * scale
+ *    exact in bf16 and in the matrix instructions.
+ * latent_dim in {256, 512}, rope_dim in {32, 64}, page_size a power of two in
+ * [8, 256]. Pools must be 16-byte aligned and have fewer than 2^31 rows.
+ */
+
+/* Parameters of paged_latent_append and paged_latent_gather. */
+typedef struct {
+  int32_t batch;             /* B >= 0 */
+  int32_t total_rows;        /* rows of the ragged tensors; row_offsets[B] <= this */
+  int32_t latent_dim;        /* 256 or 512 */
+  int32_t rope_dim;          /* 32 or 64 */
+  int32_t page_size;         /* a power of two in [8, 256] */
+  int32_t max_pages_per_seq; /* row stride of page_table */
+  int32_t num_pages;         /* pages in each pool; page ids must be < this */
+  int32_t kv_dtype;          /* PDA_KV_BF16 or PDA_KV_FP8_E4M3 */
+  int64_t latent_stride;     /* elements between rows of the ragged latent tensor
+                                (>= latent_dim, a multiple of 8) */
+  int64_t rope_stride;       /* the same for the ragged rope tensor */
+  void* latent_scales;       /* FP8: uint8 [num_pages, page_size] (written by append,
+                                read by gather); ignored otherwise */
+} pda_latent_rows_params;
+
+/*
+ * Write ragged new rows into a latent cache: row row_offsets[b] + t of
+ * (latent, rope) is written at position kv_lens[b] + t of sequence b, for
+ * every t < row_offsets[b + 1] - row_offsets[b].
+ *
+ * latent       device, bf16 [total_rows, latent_dim], row stride latent_stride.
+ * rope         device, bf16 [total_rows, rope_dim], row stride rope_stride.
+ * row_offsets  device, int32 [B + 1], not decreasing. Rows outside
+ *              [row_offsets[0], row_offsets[B]) are not read.
+ * page_table   device, int32 [B, max_pages_per_seq]; the pages covering the
+ *              new positions must already be assigned.
+ * kv_lens      device, int32 [B]: lengths before the append (read only).
+ *
+ * bf16 pools receive the bits. FP8: with a = max |x| over the latent row (NaN
+ * left out), the row's exponent is the least e in [-30, 30] with a <= 448 *
+ * 2^e, its scale byte e + 127, and its codes e4m3(x * 2^-e), nearest even,
+ * saturated to +-448 (NaN stays NaN). Only the slots of the new rows are
+ * written. If two rows name the same slot its content is unspecified.
+ *
+ * latent, rope and the pools must be 16-byte aligned, the int32 arrays 4-byte.
+ * A position past max_pages_per_seq * page_size, a negative kv_len or a page
+ * id out of range is not written and records PDA_ERR_BAD_PAGE in the device
+ * error word. Asynchronous on `stream`; no workspace.
+ */
+PDA_API pda_status paged_latent_append(const void* latent, const void* rope,
+                                       const int32_t* row_offsets, const int32_t* page_table,
+                                       const int32_t* kv_lens, const pda_latent_rows_params* params,
+                                       void* latent_pages, void* rope_pages, pda_stream_t stream);
+
+/*
+ * Read rows of a latent cache back: position starts[b] + t of sequence b goes
+ * to row row_offsets[b] + t of the ragged bf16 outputs, for every t <
+ * row_offsets[b + 1] - row_offsets[b]. FP8 rows come back as code *
+ * 2^(scale - 127), which bf16 holds exactly.
+ *
+ * starts       device, int32 [B], or NULL (every sequence from position 0).
+ * latent, rope device outputs [total_rows, ...] with the params' row strides;
+ *              rows outside [row_offsets[0], row_offsets[B]) and the gaps
+ *              between strided rows are left as they were.
+ * The rest as for paged_latent_append. A row whose position or page id is out
+ * of range is left as it was and records PDA_ERR_BAD_PAGE.
+ */
+PDA_API pda_status paged_latent_gather(const void* latent_pages, const void* rope_pages,
+                                       const int32_t* page_table, const int32_t* row_offsets,
+                                       const int32_t* starts, const pda_latent_rows_params* params,
+                                       void* latent, void* rope, pda_stream_t stream);
+
+/* Parameters of paged_latent_decode. */
+typedef struct {
+  int32_t batch;             /* B in [0, 65535] */
+  int32_t q_len;             /* query rows per sequence, 1..8 */
+  int32_t num_heads;         /* H in [1, 256] */
+  int32_t latent_dim;        /* 256 or 512 */
+  int32_t rope_dim;          /* 32 or 64 */
+  int32_t page_size;         /* a power of two in [8, 256] */
+  int32_t max_pages_per_seq; /* row stride of page_table; kv_lens[b] <= this * page_size */
+  int32_t num_pages;         /* pages in each pool; page ids must be < this */
+  float scale;               /* softmax scale (> 0) */
+  int32_t causal_offset;     /* as in pda_params */
+  int32_t window;            /* as in pda_params */
+  int32_t kv_dtype;          /* PDA_KV_BF16 or PDA_KV_FP8_E4M3 */
+  uint32_t flags;            /* PDA_FLAG_NO_PDL, or 0 */
+  const void* latent_scales; /* FP8: device uint8 [num_pages, page_size]; ignored otherwise */
+  void* workspace;           /* device scratch (any contents), or NULL */
+  size_t workspace_bytes;    /* size of workspace */
+} pda_latent_params;
+
+/*
+ * Latent decode attention in the absorbed form: for query row i and head h of
+ * sequence b, with q = [q_c | q_r],
+ *   s_j = scale * (q_c . c_j + q_r . r_j)     for every key j the row may see
+ *   lse = ln sum_j exp(s_j),   out = sum_j exp(s_j - lse) * c_j
+ * Which keys a row sees is decided as in paged_decode_attn; a row that sees
+ * none gets out = 0 and lse = -inf.
+ *
+ * q            device, bf16 [B, q_len, H, latent_dim + rope_dim], contiguous.
+ * out          device, bf16 [B, q_len, H, latent_dim] (the operand of the
+ *              value up-projection).
+ * lse          device, fp32 [B, q_len, H], natural log; may be NULL.
+ * Accumulation and softmax statistics are fp32; each weight enters the sum
+ * over values with 8 significant bits.
+ *
+ * Slots of a page past kv_lens[b] and keys no row may see are never weighted
+ * (their bytes may be NaN). q, pools and out 16-byte aligned, the rest 4-byte
+ * (latent_scales 1-byte), a caller workspace 256-byte.
+ *
+ * Workspace: paged_latent_decode_workspace_bytes(params) bytes; it holds the
+ * partial results of sequences that several CTAs share, and every slot read
+ * was written earlier in the same call. NULL: the library-owned buffer of
+ * paged_decode_attn, under the same rule for calls that may overlap; a call
+ * that is being captured into a graph must pass a workspace of its own
+ * (PDA_ERR_WORKSPACE otherwise).
+ * A page id or length out of range is never used to form an address; it
+ * records PDA_ERR_BAD_PAGE and the affected output is unspecified.
+ */
+PDA_API pda_status paged_latent_decode(const void* q, const void* latent_pages,
+                                       const void* rope_pages, const int32_t* page_table,
+                                       const int32_t* kv_lens, const pda_latent_params* params,
+                                       void* out, float* lse, pda_stream_t stream);
+
+/* Bytes of workspace paged_latent_decode needs for these params on the
+ * current device; SIZE_MAX if the params are invalid. */
+PDA_API size_t paged_latent_decode_workspace_bytes(const pda_latent_params* params);
+
+/* Parameters of latent_prefill_attn. */
+typedef struct {
+  int32_t batch;          /* B in [0, 65535] */
+  int32_t total_q;        /* rows of q; q_offsets[B] <= this */
+  int32_t total_kv;       /* rows of kv and k_rope; kv_offsets[B] <= this */
+  int32_t max_q_len;      /* host bound on the query rows of a sequence; rows past it are
+                             not computed */
+  int32_t num_heads;      /* H in [1, 256] */
+  int32_t head_dim;       /* width of k_nope and of v: 128 */
+  int32_t rope_dim;       /* 32 or 64 */
+  int64_t k_rope_stride;  /* elements between rows of k_rope (>= rope_dim, a multiple of 8) */
+  float scale;            /* softmax scale (> 0) */
+  int32_t causal_offset;  /* PDA_CAUSAL_OFF, PDA_CAUSAL_BOTTOM_RIGHT, or >= 0 */
+  int32_t window;         /* as in pda_params */
+} pda_latent_prefill_params;
+
+/*
+ * Attention over an expanded latent cache, ragged: sequence b has query rows
+ * [q_offsets[b], q_offsets[b + 1]) and keys [kv_offsets[b], kv_offsets[b + 1]);
+ * head h of key j has k = [kv[j, h, 0:D] | k_rope[j]] and v = kv[j, h, D:2D], D
+ * = head_dim, so kv is the up-projection's output as it stands. Query row i of
+ * a sequence with n_q rows and n_kv keys is at position n_kv - n_q + i
+ * (PDA_CAUSAL_BOTTOM_RIGHT), causal_offset + i (>= 0) or n_kv - 1 (off); it
+ * sees keys up to its position (causal) and within the window, as in
+ * paged_decode_attn. A row that sees no key gets out = 0 and lse = -inf.
+ *
+ * q       device, bf16 [total_q, H, D + rope_dim], contiguous.
+ * kv      device, bf16 [total_kv, H, 2 D], contiguous.
+ * k_rope  device, bf16 [total_kv, rope_dim], row stride k_rope_stride.
+ * q_offsets, kv_offsets  device, int32 [B + 1], not decreasing.
+ * out     device, bf16 [total_q, H, D];  lse  device, fp32 [total_q, H] or
+ *         NULL. Rows outside [q_offsets[0], q_offsets[B]) are left as they were.
+ * Accumulation and softmax statistics are fp32; weights are rounded to bf16.
+ * Keys that no row of a sequence may see are never weighted. All pointers but
+ * the int32 arrays and lse 16-byte aligned. Offsets out of range record
+ * PDA_ERR_BAD_PAGE and the affected output is unspecified. No workspace.
+ */
+PDA_API pda_status latent_prefill_attn(const void* q, const void* kv, const void* k_rope,
+                                       const int32_t* q_offsets, const int32_t* kv_offsets,
+                                       const pda_latent_prefill_params* params, void* out,
+                                       float* lse, pda_stream_t stream);
+
 /* Human-readable name of a status. Never NULL. */
 PDA_API const char* pda_status_string(pda_status status);
 

@@ -39,7 +39,8 @@ EXPORTED = (
     "paged_decode_attn", "paged_decode_attn_no_alloc", "paged_decode_attn_workspace_bytes",
     "pda_choose_num_splits", "pda_merge_states", "pda_status_string",
     "pda_last_device_error", "pda_abi_version", "pda_plan_kernel", "pda_hbm_read_probe",
-    "paged_kv_append",
+    "paged_kv_append", "paged_latent_append", "paged_latent_gather", "paged_latent_decode",
+    "paged_latent_decode_workspace_bytes", "latent_prefill_attn",
 )
 PDA_KERNEL_SPLIT_FMA = 0
 PDA_KERNEL_SPLIT_TMA = 1
@@ -99,6 +100,65 @@ class PdaParams(ctypes.Structure):
     ]
 
 
+class PdaLatentRowsParams(ctypes.Structure):
+    """Mirror of ``pda_latent_rows_params``."""
+
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("total_rows", ctypes.c_int32),
+        ("latent_dim", ctypes.c_int32),
+        ("rope_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("max_pages_per_seq", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("kv_dtype", ctypes.c_int32),
+        ("latent_stride", ctypes.c_int64),
+        ("rope_stride", ctypes.c_int64),
+        ("latent_scales", ctypes.c_void_p),
+    ]
+
+
+class PdaLatentParams(ctypes.Structure):
+    """Mirror of ``pda_latent_params``."""
+
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("q_len", ctypes.c_int32),
+        ("num_heads", ctypes.c_int32),
+        ("latent_dim", ctypes.c_int32),
+        ("rope_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("max_pages_per_seq", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("causal_offset", ctypes.c_int32),
+        ("window", ctypes.c_int32),
+        ("kv_dtype", ctypes.c_int32),
+        ("flags", ctypes.c_uint32),
+        ("latent_scales", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class PdaLatentPrefillParams(ctypes.Structure):
+    """Mirror of ``pda_latent_prefill_params``."""
+
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("total_q", ctypes.c_int32),
+        ("total_kv", ctypes.c_int32),
+        ("max_q_len", ctypes.c_int32),
+        ("num_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("rope_dim", ctypes.c_int32),
+        ("k_rope_stride", ctypes.c_int64),
+        ("scale", ctypes.c_float),
+        ("causal_offset", ctypes.c_int32),
+        ("window", ctypes.c_int32),
+    ]
+
+
 _lib = None
 
 
@@ -137,6 +197,19 @@ def load(path: Optional[str] = None):
     lib.paged_kv_append.argtypes = [vp, vp, vp, vp, ctypes.POINTER(PdaAppendParams), vp, vp, vp]
     lib.pda_hbm_read_probe.restype = i32
     lib.pda_hbm_read_probe.argtypes = [vp, ctypes.c_size_t, vp, vp]
+    rp = ctypes.POINTER(PdaLatentRowsParams)
+    lib.paged_latent_append.restype = i32
+    lib.paged_latent_append.argtypes = [vp, vp, vp, vp, vp, rp, vp, vp, vp]
+    lib.paged_latent_gather.restype = i32
+    lib.paged_latent_gather.argtypes = [vp, vp, vp, vp, vp, rp, vp, vp, vp]
+    lp = ctypes.POINTER(PdaLatentParams)
+    lib.paged_latent_decode.restype = i32
+    lib.paged_latent_decode.argtypes = [vp, vp, vp, vp, vp, lp, vp, vp, vp]
+    lib.paged_latent_decode_workspace_bytes.restype = ctypes.c_size_t
+    lib.paged_latent_decode_workspace_bytes.argtypes = [lp]
+    lib.latent_prefill_attn.restype = i32
+    lib.latent_prefill_attn.argtypes = [vp, vp, vp, vp, vp, ctypes.POINTER(PdaLatentPrefillParams),
+                                        vp, vp, vp]
     if path is None:
         _lib = lib
     return lib
@@ -349,6 +422,208 @@ def merge_states(o_parts, lse_parts, *, out=None, lse=None, sinks=None, stream=N
                                  0 if sinks is None else sinks.numel(), _stream_handle(stream))
     if st != 0:
         raise PdaError(st, "pda_merge_states")
+    return out, lse
+
+
+def _check(name, t, dtype, shape, device, rows=False):
+    """Raise ValueError unless t is a CUDA tensor of this type and shape on
+    `device`, contiguous (``rows``: unit stride within a row is enough; None in
+    `shape` matches any size)."""
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if not (t.is_contiguous() or (rows and (t.shape[-1] <= 1 or t.stride(-1) == 1))):
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _on_current_device(device):
+    """The library works on the current device: refuse tensors of another."""
+    import torch
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}, which is not the current CUDA device")
+
+
+def _used_on(stream, *tensors):
+    """Tell the allocator that `stream` uses tensors made on the current one."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _row_stride(t):
+    """Elements between the rows of a [rows, width] tensor (one row has none:
+    its width, which any row count accepts)."""
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 7) // 8 * 8
+
+
+def _latent_pools(latent_pages, rope_pages, latent_scales, page_table):
+    """Check the pools of a latent cache and its page table; the KV dtype."""
+    import torch
+    dev = latent_pages.device
+    fp8 = latent_pages.dtype == torch.uint8
+    _check("latent_pages", latent_pages, torch.uint8 if fp8 else torch.bfloat16,
+           (None, None, None), dev)
+    pools = tuple(latent_pages.shape[:2])
+    _check("rope_pages", rope_pages, torch.bfloat16, pools + (None,), dev)
+    _check("page_table", page_table, torch.int32, (None, None), dev)
+    if fp8:
+        if latent_scales is None:
+            raise ValueError("uint8 latent_pages need latent_scales")
+        _check("latent_scales", latent_scales, torch.uint8, pools, dev)
+    elif latent_scales is not None:
+        raise ValueError("latent_scales go with uint8 latent_pages")
+    return PDA_KV_FP8_E4M3 if fp8 else PDA_KV_BF16
+
+
+def _latent_rows(latent, rope, row_offsets, page_table, starts, latent_pages, rope_pages,
+                 latent_scales):
+    import torch
+    kv_dtype = _latent_pools(latent_pages, rope_pages, latent_scales, page_table)
+    _on_current_device(latent_pages.device)
+    dev, (num_pages, page, width), batch = latent_pages.device, latent_pages.shape, page_table.shape[0]
+    rope_dim, rows = rope_pages.shape[2], latent.shape[0]
+    _check("latent", latent, torch.bfloat16, (rows, width), dev, rows=True)
+    _check("rope", rope, torch.bfloat16, (rows, rope_dim), dev, rows=True)
+    _check("row_offsets", row_offsets, torch.int32, (batch + 1,), dev)
+    if starts is not None:
+        _check("kv_lens / starts", starts, torch.int32, (batch,), dev)
+    return PdaLatentRowsParams(batch, rows, width, rope_dim, page, page_table.shape[1], num_pages,
+                               kv_dtype, _row_stride(latent), _row_stride(rope), _ptr(latent_scales))
+
+
+def paged_latent_append(latent, rope, row_offsets, page_table, kv_lens, latent_pages, rope_pages,
+                        *, latent_scales=None, stream=None):
+    """Write ragged new rows into a latent cache: rows row_offsets[b] ..
+    row_offsets[b + 1] of latent (bf16 [rows, R]) and rope (bf16 [rows, Dr])
+    go to positions kv_lens[b], kv_lens[b] + 1, ... of sequence b (kv_lens is
+    not advanced). latent_pages [num_pages, P, R] bf16 takes the bits; uint8
+    takes e4m3 codes, and latent_scales (uint8 [num_pages, P]) each row's
+    power-of-two scale. latent and rope may be column slices of one tensor."""
+    p = _latent_rows(latent, rope, row_offsets, page_table, kv_lens, latent_pages, rope_pages,
+                     latent_scales)
+    st = load().paged_latent_append(_ptr(latent), _ptr(rope), _ptr(row_offsets), _ptr(page_table),
+                                    _ptr(kv_lens), ctypes.byref(p), _ptr(latent_pages),
+                                    _ptr(rope_pages), _stream_handle(stream))
+    if st != 0:
+        raise PdaError(st, "paged_latent_append")
+
+
+def paged_latent_gather(latent_pages, rope_pages, page_table, row_offsets, *, total_rows=None,
+                        starts=None, latent_scales=None, latent=None, rope=None, stream=None):
+    """Read rows of a latent cache back as bf16: positions starts[b] (default
+    0), starts[b] + 1, ... of sequence b become rows row_offsets[b] ..
+    row_offsets[b + 1] of the outputs. Returns (latent [rows, R], rope [rows,
+    Dr]): the given ones (rows behind row_offsets[B] are left alone), or new
+    ones of total_rows rows."""
+    import torch
+    if latent is None or rope is None:
+        if total_rows is None:
+            raise ValueError("total_rows is needed to allocate the outputs")
+        if latent is None:
+            latent = torch.empty((total_rows, latent_pages.shape[2]), dtype=torch.bfloat16,
+                                 device=latent_pages.device)
+        if rope is None:
+            rope = torch.empty((total_rows, rope_pages.shape[2]), dtype=torch.bfloat16,
+                               device=latent_pages.device)
+    p = _latent_rows(latent, rope, row_offsets, page_table, starts, latent_pages, rope_pages,
+                     latent_scales)
+    st = load().paged_latent_gather(_ptr(latent_pages), _ptr(rope_pages), _ptr(page_table),
+                                    _ptr(row_offsets), _ptr(starts), ctypes.byref(p), _ptr(latent),
+                                    _ptr(rope), _stream_handle(stream))
+    if st != 0:
+        raise PdaError(st, "paged_latent_gather")
+    _used_on(stream, latent, rope)
+    return latent, rope
+
+
+def paged_latent_decode(q, latent_pages, rope_pages, page_table, kv_lens, *, scale,
+                        causal_offset=PDA_CAUSAL_OFF, window=0, latent_scales=None, out=None,
+                        lse=None, with_lse=True, workspace=None, library_workspace=False, flags=0,
+                        stream=None):
+    """Decode attention over a latent cache in the absorbed form; returns
+    (out, lse). q bf16 [B, q_len, H, R + Dr] holds each head's query against
+    the latents and its rotated part; out bf16 [B, q_len, H, R] is the weighted
+    sum of latents, lse fp32 [B, q_len, H]. Pools as for paged_latent_append;
+    masks and workspace as for paged_decode_attn."""
+    import torch
+    lib = load()
+    kv_dtype = _latent_pools(latent_pages, rope_pages, latent_scales, page_table)
+    _on_current_device(q.device)
+    dev, (num_pages, page, width) = q.device, latent_pages.shape
+    rope_dim = rope_pages.shape[2]
+    _check("q", q, torch.bfloat16, (None, None, None, width + rope_dim), latent_pages.device)
+    B, q_len, H, _ = q.shape
+    _check("page_table", page_table, torch.int32, (B, None), dev)
+    _check("kv_lens", kv_lens, torch.int32, (B,), dev)
+    if out is None:
+        out = torch.empty((B, q_len, H, width), dtype=torch.bfloat16, device=dev)
+    else:
+        _check("out", out, torch.bfloat16, (B, q_len, H, width), dev)
+    if lse is None and with_lse:
+        lse = torch.empty((B, q_len, H), dtype=torch.float32, device=dev)
+    elif lse is not None:
+        _check("lse", lse, torch.float32, (B, q_len, H), dev)
+    p = PdaLatentParams(B, q_len, H, width, rope_dim, page, page_table.shape[1], num_pages, scale,
+                        causal_offset, window, kv_dtype, flags, _ptr(latent_scales), None, 0)
+    if workspace is None and not library_workspace:
+        need = lib.paged_latent_decode_workspace_bytes(ctypes.byref(p))
+        if need == ctypes.c_size_t(-1).value:
+            raise PdaError(1, "paged_latent_decode_workspace_bytes")
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if workspace is not None:
+        p.workspace = workspace.data_ptr()
+        p.workspace_bytes = workspace.numel() * workspace.element_size()
+    st = lib.paged_latent_decode(_ptr(q), _ptr(latent_pages), _ptr(rope_pages), _ptr(page_table),
+                                 _ptr(kv_lens), ctypes.byref(p), _ptr(out), _ptr(lse),
+                                 _stream_handle(stream))
+    if st != 0:
+        raise PdaError(st, "paged_latent_decode")
+    _used_on(stream, out, lse, workspace)
+    return out, lse
+
+
+def latent_prefill_attn(q, kv, k_rope, q_offsets, kv_offsets, *, scale,
+                        causal_offset=PDA_CAUSAL_BOTTOM_RIGHT, window=0, max_q_len=None, out=None,
+                        lse=None, with_lse=True, stream=None):
+    """Attention over an expanded latent cache, ragged; returns (out, lse).
+    q bf16 [total_q, H, D + Dr]; kv bf16 [total_kv, H, 2 D], each head's keys
+    then its values (the up-projection's output); k_rope bf16 [total_kv, Dr],
+    shared by the heads; q_offsets, kv_offsets int32 [B + 1]. ``max_q_len``:
+    a bound on the query rows of a sequence (default total_q; a tighter one
+    launches fewer idle CTAs). out bf16 [total_q, H, D], lse fp32 [total_q, H]."""
+    import torch
+    lib = load()
+    dev = q.device
+    _on_current_device(dev)
+    _check("q", q, torch.bfloat16, (None, None, None), dev)
+    total_q, H, width = q.shape
+    _check("kv", kv, torch.bfloat16, (None, H, None), dev)
+    total_kv, D = kv.shape[0], kv.shape[2] // 2
+    _check("kv", kv, torch.bfloat16, (None, H, 2 * D), dev)
+    _check("k_rope", k_rope, torch.bfloat16, (total_kv, width - D), dev, rows=True)
+    _check("q_offsets", q_offsets, torch.int32, (None,), dev)
+    B = q_offsets.shape[0] - 1
+    _check("kv_offsets", kv_offsets, torch.int32, (B + 1,), dev)
+    if out is None:
+        out = torch.empty((total_q, H, D), dtype=torch.bfloat16, device=dev)
+    else:
+        _check("out", out, torch.bfloat16, (total_q, H, D), dev)
+    if lse is None and with_lse:
+        lse = torch.empty((total_q, H), dtype=torch.float32, device=dev)
+    elif lse is not None:
+        _check("lse", lse, torch.float32, (total_q, H), dev)
+    p = PdaLatentPrefillParams(B, total_q, total_kv, total_q if max_q_len is None else max_q_len, H,
+                               D, width - D, _row_stride(k_rope), scale, causal_offset, window)
+    st = lib.latent_prefill_attn(_ptr(q), _ptr(kv), _ptr(k_rope), _ptr(q_offsets), _ptr(kv_offsets),
+                                 ctypes.byref(p), _ptr(out), _ptr(lse), _stream_handle(stream))
+    if st != 0:
+        raise PdaError(st, "latent_prefill_attn")
+    _used_on(stream, out, lse)
     return out, lse
 
 
