@@ -5,118 +5,17 @@
 #include <cmath>
 #include <cstdint>
 
+#include "latent_decode.h"
 #include "paged_decode_attn.h"
-#include "pda_device.cuh"
 
 namespace pda {
 
-int* device_error_word();  // paged_decode_attn.cu
+// paged_decode_attn.cu
+int* device_error_word();
+int device_sms();
+pda_status library_workspace(size_t bytes, cudaStream_t stream, void** out);
 
 namespace {
-
-struct LatentArgs {
-  const uint16_t* q;  // bf16 [B, q_len, H, R + rope_dim]
-  const uint8_t* latent_pages;
-  const uint16_t* rope_pages;
-  const uint8_t* scales;
-  const int32_t* page_table;
-  const int32_t* kv_lens;
-  uint16_t* out;
-  float* lse;
-  int* err;
-  int B, Lq, H, M, rope_dim, page_size, log2_page, max_pages, num_pages, causal_offset, window;
-  float scale_log2;
-};
-
-// Keys [lo, hi) that query row i of a sequence of L keys sees.
-__device__ __forceinline__ void visible(const LatentArgs& a, int L, int i, int& lo, int& hi) {
-  long long pos = (long long)L - 1;
-  if (a.causal_offset >= 0) pos = (long long)a.causal_offset + i;
-  else if (a.causal_offset == -2) pos = (long long)L - a.Lq + i;
-  long long h = a.causal_offset != -1 ? pos + 1 : (long long)L;
-  long long l = a.window > 0 ? pos - a.window + 1 : 0;
-  hi = (int)(h < 0 ? 0 : (h > L ? L : h));
-  lo = (int)(l < 0 ? 0 : (l > L ? L : l));
-}
-
-// One warp per query row: walks the row's keys one by one, lanes over the
-// elements, with a running maximum and sum.
-template <int R, bool FP8>
-__global__ void __launch_bounds__(256) latent_decode_simple(const LatentArgs a) {
-  constexpr int C = R / 256;
-  constexpr unsigned FULL = 0xFFFFFFFFu;
-  const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (row >= (long long)a.B * a.M) return;
-  const int b = (int)(row / a.M), i = (int)(row % a.M) / a.H;
-  int L = __ldg(a.kv_lens + b);
-  const int Lmax = a.max_pages * a.page_size;
-  if (L < 0 || L > Lmax) {
-    if (lane == 0) record_error_at(a.err, kErrBadPage);
-    L = L < 0 ? 0 : Lmax;
-  }
-  int lo, hi;
-  visible(a, L, i, lo, hi);
-  const uint16_t* qr = a.q + row * (R + a.rope_dim);
-  const bool has_rope = lane * 8 < a.rope_dim;
-  float q[C][8], qe[8] = {}, o[C][8] = {};
-#pragma unroll
-  for (int c = 0; c < C; ++c) bf16x8_to_f32(*reinterpret_cast<const uint4*>(qr + (lane + 32 * c) * 8), q[c]);
-  if (has_rope) bf16x8_to_f32(*reinterpret_cast<const uint4*>(qr + R + lane * 8), qe);
-  float m = -INFINITY, l = 0.f;
-  for (int j = lo; j < hi; ++j) {
-    const int page = __ldg(a.page_table + (long long)b * a.max_pages + (j >> a.log2_page));
-    if ((unsigned)page >= (unsigned)a.num_pages) {
-      if (lane == 0) record_error_at(a.err, kErrBadPage);
-      continue;
-    }
-    const long long slot = (long long)page * a.page_size + (j & (a.page_size - 1));
-    float v[C][8], s = 0.f;
-    float sc = 1.f;
-    if constexpr (FP8) sc = __int_as_float(min(max((int)a.scales[slot], 97), 157) << 23);
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      if constexpr (FP8)
-        e4m3x8_to_f32(*reinterpret_cast<const uint2*>(a.latent_pages + slot * R + (lane + 32 * c) * 8), v[c]);
-      else
-        bf16x8_to_f32(*reinterpret_cast<const uint4*>(a.latent_pages + (slot * R + (lane + 32 * c) * 8) * 2), v[c]);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        v[c][k] *= sc;
-        s = fmaf(q[c][k], v[c][k], s);
-      }
-    }
-    if (has_rope) {
-      float e[8];
-      bf16x8_to_f32(*reinterpret_cast<const uint4*>(a.rope_pages + slot * a.rope_dim + lane * 8), e);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) s = fmaf(qe[k], e[k], s);
-    }
-#pragma unroll
-    for (int x = 16; x >= 1; x >>= 1) s += __shfl_xor_sync(FULL, s, x);
-    s *= a.scale_log2;
-    const float m_new = fmaxf(m, s);
-    const float alpha = m == -INFINITY ? 0.f : exp2f(m - m_new), p = s == -INFINITY ? 0.f : exp2f(s - m_new);
-    m = m_new;
-    l = l * alpha + p;
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) o[c][k] = fmaf(o[c][k], alpha, p * v[c][k]);
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    uint32_t w[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(o[c][2 * k] * inv, o[c][2 * k + 1] * inv);
-      w[k] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    *reinterpret_cast<uint4*>(a.out + row * R + (lane + 32 * c) * 8) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-  if (lane == 0 && a.lse) a.lse[row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
-}
 
 pda_status validate(const pda_latent_params* p) {
   if (p == nullptr) return PDA_ERR_INVALID_ARG;
@@ -138,6 +37,32 @@ pda_status validate(const pda_latent_params* p) {
   return PDA_OK;
 }
 
+// Launch shape and workspace of a call.
+struct Plan {
+  int nt, row_tiles, teams;
+  size_t lse_off, cut_off, total;  // the partial outputs come first
+};
+
+Plan make_plan(const pda_latent_params& p, int sms) {
+  Plan pl{};
+  const int M = p.q_len * p.num_heads;
+  const bool fp8 = p.kv_dtype == PDA_KV_FP8_E4M3;
+  // As many packed rows per CTA as TMEM (FP8: two terms a row, 32) or shared
+  // memory (bf16: 64) take, no more than there are.
+  pl.nt = M <= 16 ? 16 : (M <= 32 || fp8) ? 32 : 64;
+  pl.row_tiles = (M + pl.nt - 1) / pl.nt;
+  // One CTA per SM; a team walks a range of tokens with a CTA per row tile.
+  // Never more teams than tiles.
+  const long long tiles = (long long)p.batch * (((long long)p.max_pages_per_seq * p.page_size + 127) / 128);
+  const long long teams = sms / pl.row_tiles;
+  pl.teams = (int)(teams < 1 ? 1 : teams < tiles ? teams : tiles);
+  const size_t slots = (size_t)pl.teams * pl.row_tiles * 2 * pl.nt;
+  pl.lse_off = slots * p.latent_dim * sizeof(float);
+  pl.cut_off = (pl.lse_off + slots * sizeof(float) + 255) / 256 * 256;
+  pl.total = pl.cut_off + (size_t)pl.teams * 2 * sizeof(int);
+  return pl;
+}
+
 bool al(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 }  // namespace
@@ -149,7 +74,9 @@ extern "C" {
 
 size_t paged_latent_decode_workspace_bytes(const pda_latent_params* params) {
   if (validate(params) != PDA_OK) return SIZE_MAX;
-  return 0;
+  if (params->batch == 0) return 0;
+  const int sms = device_sms();
+  return make_plan(*params, sms > 0 ? sms : 148).total;
 }
 
 pda_status paged_latent_decode(const void* q, const void* latent_pages, const void* rope_pages,
@@ -166,39 +93,36 @@ pda_status paged_latent_decode(const void* q, const void* latent_pages, const vo
   if (!al(q, 16) || !al(latent_pages, 16) || !al(rope_pages, 16) || !al(out, 16) ||
       !al(page_table, 4) || !al(kv_lens, 4) || !al(lse, 4) || !al(p.workspace, 256))
     return PDA_ERR_MISALIGNED;
-  LatentArgs a{};
-  a.q = static_cast<const uint16_t*>(q);
-  a.latent_pages = static_cast<const uint8_t*>(latent_pages);
-  a.rope_pages = static_cast<const uint16_t*>(rope_pages);
-  a.scales = static_cast<const uint8_t*>(p.latent_scales);
-  a.page_table = page_table;
-  a.kv_lens = kv_lens;
-  a.out = static_cast<uint16_t*>(out);
-  a.lse = lse;
-  a.err = device_error_word();
-  if (a.err == nullptr) return PDA_ERR_CUDA;
-  a.B = p.batch;
-  a.Lq = p.q_len;
-  a.H = p.num_heads;
-  a.M = p.q_len * p.num_heads;
-  a.rope_dim = p.rope_dim;
-  a.page_size = p.page_size;
-  while ((1 << a.log2_page) < p.page_size) ++a.log2_page;
-  a.max_pages = p.max_pages_per_seq;
-  a.num_pages = p.num_pages;
-  a.causal_offset = p.causal_offset;
-  a.window = p.window;
-  a.scale_log2 = p.scale * 1.4426950408889634f;
+  LatentCall c{};
+  c.err = device_error_word();
+  const int sms = device_sms();
+  if (c.err == nullptr || sms < 1) return PDA_ERR_CUDA;
+  const Plan pl = make_plan(p, sms);
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-  const unsigned grid = (unsigned)(((long long)a.B * a.M + 7) / 8);
-  if (p.latent_dim == 512) {
-    if (fp8) latent_decode_simple<512, true><<<grid, 256, 0, stream>>>(a);
-    else latent_decode_simple<512, false><<<grid, 256, 0, stream>>>(a);
-  } else {
-    if (fp8) latent_decode_simple<256, true><<<grid, 256, 0, stream>>>(a);
-    else latent_decode_simple<256, false><<<grid, 256, 0, stream>>>(a);
+  void* ws = p.workspace;
+  if (ws == nullptr) {
+    if ((st = library_workspace(pl.total, stream, &ws)) != PDA_OK) return st;
+  } else if (p.workspace_bytes < pl.total) {
+    return PDA_ERR_WORKSPACE;
   }
-  return cudaGetLastError() == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
+  char* base = static_cast<char*>(ws);
+  c.p = &p;
+  c.q = q;
+  c.latent_pages = latent_pages;
+  c.rope_pages = rope_pages;
+  c.page_table = page_table;
+  c.kv_lens = kv_lens;
+  c.out = out;
+  c.lse = lse;
+  c.o_part = reinterpret_cast<float*>(base);
+  c.lse_part = reinterpret_cast<float*>(base + pl.lse_off);
+  c.cut = base + pl.cut_off;
+  c.nt = pl.nt;
+  c.row_tiles = pl.row_tiles;
+  c.teams = pl.teams;
+  const cudaError_t e = fp8 ? launch_latent_decode_fp8(c, stream) : launch_latent_decode_bf16(c, stream);
+  if (e == cudaErrorNotSupported) return PDA_ERR_UNSUPPORTED;
+  return e == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
 }
 
 }  // extern "C"

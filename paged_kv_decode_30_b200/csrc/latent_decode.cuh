@@ -1,0 +1,905 @@
+// Latent decode attention in the absorbed form on the 5th-generation tensor
+// cores: q = [q_c | q_r] of every head against the latent rows [c | r] of a
+// sequence's pages, values c.
+//
+// A latent row is key and value at once and serves all heads, so the packed
+// query rows (q_len x heads, NT of them per CTA) share every byte read. Per
+// tile of 128 tokens, tokens are the M dimension of both products:
+//   S^T [128 tokens, NT] = C Q_c^T + R Q_r^T   (K: R + 64 elements)
+//   O^T [R dims, NT]    += C^T P^T             (K: 128 tokens; R / 128 blocks)
+// The tile C enters both from the same shared memory: K-major for S^T and
+// MN-major for O^T. O^T stays in TMEM over a sequence; NT is bounded by TMEM
+// (512 columns) and by shared memory (Q and one to two tiles).
+//
+// Bounds: a tile brings 128 x (2R + 2 rope) bytes (FP8: R + 2 rope) for 2 x
+// 128 x NT x (2R + rope) operations. At R = 512 and 64 rows or fewer HBM is
+// the bound; with more rows several CTAs take the same tiles (row tiles), the
+// later ones from L2, and the matrix products and the shared memory they are
+// fed from become the bound.
+//
+// Schedule: the tiles of all sequences form one line, cut into equal ranges
+// for `teams` teams; the CTAs of a team take the same range for one row tile
+// each, at the same time, so that HBM sees each tile once. A sequence that
+// lies in one range is finished by its CTA; one that is cut leaves partial
+// results that a second kernel joins. The ranges follow from kv_lens by a scan
+// that every CTA makes for itself: no counters, no atomics, one order of sums.
+//
+// FP8 rows are e4m3 codes with a power-of-two scale 2^e a row. Codes go to the
+// matrix instructions as they are (kind::f8f6f4); a bf16 query row times a
+// power of two is the exact sum of two e4m3 terms [hi; 16 lo]; the rotated
+// parts are bf16 products into columns of their own. With x_j the score
+// (log2 units) the weight is w_j = 2^(x_j + e_j - m), m a running maximum of
+// x + e, split in two e4m3 terms as well; the normaliser adds w_j 2^-e_j.
+//
+// Roles (warps): 0 TMA producer, 1 S^T issuer, 2 O^T issuer, 3 schedule,
+// 4.. softmax (NT / 16 groups of four warps, 16 rows a thread, thread = token
+// of S^T = element of an O^T block). Every wait is bounded.
+#pragma once
+
+#include "pda_device.cuh"
+#include "split_tma.cuh"  // MMA issue, instruction descriptors, TMA loads, e4m3 splits
+#include "tcgen05.cuh"
+
+namespace pda {
+
+struct LatentArgs {
+  const uint16_t* q;  // bf16 [B, M, R + rope_dim], M = q_len * H
+  const uint8_t* scales;
+  const int32_t* page_table;
+  const int32_t* kv_lens;
+  uint16_t* out;  // bf16 [B, M, R]
+  float* lse;     // [B, M] or null
+  int* err;
+  float* o_part;    // [teams * row_tiles * 2][NT][R]
+  float* lse_part;  // [teams * row_tiles * 2][NT]
+  int2* cut;        // [teams]: (sequence, last team) of the cut sequence that starts in the team
+  int B, Lq, H, M, rope_dim, page_size, log2_page, max_pages, num_pages, causal_offset, window;
+  int teams, row_tiles;
+  float scale_log2;
+};
+
+constexpr int kTile = 128;
+
+// Keys [lo, hi) that query row i of a sequence of L keys sees.
+__device__ __forceinline__ void latent_visible(const LatentArgs& a, int L, int i, int& lo, int& hi) {
+  long long pos = (long long)L - 1;
+  if (a.causal_offset >= 0) pos = (long long)a.causal_offset + i;
+  else if (a.causal_offset == -2) pos = (long long)L - a.Lq + i;
+  const long long h = a.causal_offset != -1 ? pos + 1 : (long long)L;
+  const long long l = a.window > 0 ? pos - a.window + 1 : 0;
+  hi = (int)(h < 0 ? 0 : (h > L ? L : h));
+  lo = (int)(l < 0 ? 0 : (l > L ? L : l));
+}
+
+__device__ __forceinline__ int latent_len(const LatentArgs& a, int b) {
+  return min(max(__ldg(a.kv_lens + b), 0), a.max_pages << a.log2_page);
+}
+
+// First tile and number of tiles that any query row of the sequence sees.
+__device__ __forceinline__ void latent_tiles(const LatentArgs& a, int L, int& first, int& n) {
+  int lo, hi, x;
+  latent_visible(a, L, 0, lo, x);
+  latent_visible(a, L, a.Lq - 1, x, hi);
+  first = lo / kTile;
+  n = hi > lo ? (hi + kTile - 1) / kTile - first : 0;
+}
+
+// A sequence's share of the line: its tiles, and one unit if it has none, so
+// that some CTA writes its rows.
+__device__ __forceinline__ int latent_weight(const LatentArgs& a, int b) {
+  int first, n;
+  latent_tiles(a, latent_len(a, b), first, n);
+  return max(n, 1);
+}
+
+struct LatentItem {
+  int b;              // < 0: no more items
+  int L, first, n;    // kv length, first tile, tiles
+  int part;           // slot of the partial results, -1: the sequence is finished here
+  int lo_u, hi_u;     // keys that some row of the row tile sees
+  int lo_x, hi_x;     // keys that all rows of it see
+  int pad[3];
+};
+
+template <int R_, bool FP8_, int NT_>
+struct LatentCfg {
+  static constexpr int R = R_, NT = NT_, NB = R / 128;
+  static constexpr bool FP8 = FP8_;
+  static constexpr int HALF = kTile * 128;              // a 128-byte column of a tile
+  static constexpr int BLK = FP8 ? HALF : 2 * HALF;     // 128 elements of a tile's rows
+  static constexpr int N1 = FP8 ? 2 * NT : NT;          // S^T columns of the latent product
+  static constexpr int N2 = FP8 ? 2 * NT : NT;          // O^T columns of a block
+  static constexpr int SN = FP8 ? 3 * NT : NT;          // S^T columns (FP8: rotated part apart)
+  // Q operand, K-major: FP8 per block [hi; lo] rows of 128 codes, bf16 per 64
+  // elements NT rows; then the rotated part, NT rows of 64 bf16.
+  static constexpr int Q_BLK = FP8 ? N1 * 128 : 2 * NT * 128;
+  static constexpr int Q_ROPE = NB * Q_BLK;
+  static constexpr int Q_BYTES = Q_ROPE + NT * 128;
+  static constexpr int P_ROW = 2 * NT;                  // bytes of a token's weights
+  static constexpr int P_BYTES = kTile * P_ROW;
+  static constexpr uint32_t P_SWIZZLE = P_ROW == 128 ? kSw128 : P_ROW == 64 ? kSw64 : kSw32;
+  // Shared memory is Q, weights, the rotated parts' slot and as many 128-element
+  // blocks of latents as fit. The widest bf16 case has room for one tile only
+  // if the weights take the place of the rotated parts, which the S^T product
+  // has read by then.
+  static constexpr bool OVERLAY = !FP8 && NT == 64 && R == 512;
+  static constexpr int P_BUFS = (OVERLAY || (!FP8 && NT == 32 && R == 512)) ? 1 : 2;
+  static constexpr int R_SLOTS = FP8 ? 2 : 1;
+  static constexpr int ROPE_SLOT = HALF;
+  static constexpr int STATE = 16 * NT * 4 + 1024;
+  static constexpr int FREE = 227 * 1024 - 1024 - STATE - Q_BYTES - (OVERLAY ? 0 : P_BUFS * P_BYTES) -
+                              R_SLOTS * ROPE_SLOT;
+  static constexpr int SLOTS = FREE / BLK < 3 * NB ? FREE / BLK : 3 * NB;
+  static constexpr int OFF_BLK = 0;
+  static constexpr int OFF_ROPE = OFF_BLK + SLOTS * BLK;
+  static constexpr int OFF_Q = OFF_ROPE + R_SLOTS * ROPE_SLOT;
+  static constexpr int OFF_P = OVERLAY ? OFF_ROPE : OFF_Q + Q_BYTES;
+  static constexpr int OFF_STATE = OVERLAY ? OFF_Q + Q_BYTES : OFF_P + P_BUFS * P_BYTES;
+  static constexpr int OFF_M = OFF_STATE;               // running maximum per row
+  static constexpr int OFF_ALPHA = OFF_M + NT * 4;
+  static constexpr int OFF_WMAX = OFF_ALPHA + NT * 4;   // [4][NT]
+  static constexpr int OFF_LRED = OFF_WMAX + 4 * NT * 4;   // [4][NT]: also the rounded sums'
+  static constexpr int OFF_INV = OFF_LRED + 4 * NT * 4;
+  static constexpr int OFF_CS = OFF_INV + NT * 4;       // score scale per row (FP8)
+  static constexpr int OFF_RANGE = OFF_CS + NT * 4;     // int2 visible keys per row
+  static constexpr int OFF_ITEM = OFF_RANGE + NT * 8;
+  static constexpr int ITEMS = 4;
+  static constexpr int OFF_BAR = OFF_ITEM + ITEMS * (int)sizeof(LatentItem);
+  static constexpr int BARS = 2 * SLOTS + 2 * R_SLOTS + 2 + 2 + 2 + 3 + 2 * ITEMS;
+  static constexpr int OFF_MISC = OFF_BAR + BARS * 8;   // TMEM address, abort flag, scan sums
+  static constexpr int SMEM = OFF_MISC + 16 + 32 * 8;
+  static constexpr int SMEM_ALLOC = SMEM + 1024;
+  static constexpr int GROUPS = NT / 16;
+  static constexpr int SOFT = 4;                        // first softmax warp
+  static constexpr int WARPS = SOFT + 4 * GROUPS;
+  static constexpr int THREADS = 32 * WARPS;
+  static constexpr int SOFT_THREADS = 128 * GROUPS;
+  static constexpr int COL_O = 0, COL_S = NB * N2;
+  static constexpr int COLS = COL_S + 2 * SN;
+  static constexpr int TMEM_COLS = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+  static_assert(COLS <= 512 && SLOTS >= NB && SMEM_ALLOC <= 227 * 1024, "capacity");
+  static_assert(BLK % 1024 == 0 && Q_BLK % 1024 == 0 && Q_BYTES % 1024 == 0 && P_BYTES % 1024 == 0, "alignment");
+  // Weights are at most 2^8 (e4m3 holds 448). FP8 starts them at 2^4, which
+  // keeps the second term's smallest step 2^18 below the largest weight.
+  static constexpr float HEAD = FP8 ? 4.f : 0.f;
+};
+
+// 128-byte-swizzled address of 16-byte piece c of row n in a block of rows.
+__device__ __forceinline__ uint32_t sw128(int n, int c) {
+  return (n >> 3) * 1024 + (n & 7) * 128 + ((c ^ (n & 7)) << 4);
+}
+
+template <int R, bool FP8, int NT>
+__global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
+    latent_decode_kernel(const __grid_constant__ CUtensorMap map_c,
+                         const __grid_constant__ CUtensorMap map_r,
+                         const __grid_constant__ CUtensorMap map_q, const LatentArgs a) {
+  using C = LatentCfg<R, FP8, NT>;
+  constexpr unsigned FULL = 0xFFFFFFFFu;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = smem_addr(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int team = blockIdx.x / a.row_tiles, rt = blockIdx.x % a.row_tiles;
+
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // [SLOTS] latents landed
+  uint64_t* empty = full + C::SLOTS;         // [SLOTS] O^T of the block done
+  uint64_t* rfull = empty + C::SLOTS;        // [R_SLOTS] rotated parts landed
+  uint64_t* rempty = rfull + C::R_SLOTS;     // [R_SLOTS] and read (overlay: and the weights too)
+  uint64_t* s_full = rempty + C::R_SLOTS;    // [2] S^T in TMEM
+  uint64_t* p_ready = s_full + 2;            // [2] S^T read, weights in shared memory
+  uint64_t* o_full = p_ready + 2;            // [2] O^T of the tile added
+  uint64_t* q_full = o_full + 2;             // Q of the item in shared memory
+  uint64_t* q_free = q_full + 1;             // S^T products of the item done
+  uint64_t* o_free = q_free + 1;             // O^T of the item read back
+  uint64_t* item_full = o_free + 1;          // [ITEMS]
+  uint64_t* item_free = item_full + C::ITEMS;  // [ITEMS]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  long long* sums = reinterpret_cast<long long*>(smem + C::OFF_MISC + 16);  // [WARPS]
+  LatentItem* items = reinterpret_cast<LatentItem*>(smem + C::OFF_ITEM);
+
+  if (tid == 0) {
+    for (int s = 0; s < C::SLOTS; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < C::R_SLOTS; ++s) {
+      mbar_init(&rfull[s], 1);
+      mbar_init(&rempty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_ready[s], C::SOFT_THREADS);
+      mbar_init(&o_full[s], 1);
+    }
+    mbar_init(q_full, FP8 ? C::SOFT_THREADS : 1);
+    mbar_init(q_free, 1);
+    mbar_init(o_free, C::SOFT_THREADS);
+    for (int s = 0; s < C::ITEMS; ++s) {
+      mbar_init(&item_full[s], 32);
+      mbar_init(&item_free[s], C::GROUPS + 3);  // softmax groups, producer, both MMA issuers
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(tmem_slot)),
+                 "r"(C::TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  // Each warp adds up one chunk of the sequences' weights.
+  const int chunk = (a.B + C::WARPS - 1) / C::WARPS;
+  {
+    long long w = 0;
+    for (int b = warp * chunk + lane; b < min(a.B, (warp + 1) * chunk); b += 32) {
+      w += latent_weight(a, b);
+      const int L = __ldg(a.kv_lens + b);
+      if (blockIdx.x == 0 && (L < 0 || L > (a.max_pages << a.log2_page))) record_error_at(a.err, kErrBadPage);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) w += __shfl_xor_sync(FULL, w, o);
+    if (lane == 0) sums[warp] = w;
+  }
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 3) {
+    // ======================= schedule (whole warp) =============================
+    // The line's length and this team's range [s, e) of it (a line shorter than
+    // the number of teams leaves the last ones idle, so that no range is empty);
+    // then every sequence that overlaps the range becomes an item.
+    long long total = 0;
+    for (int w = 0; w < C::WARPS; ++w) total += sums[w];
+    const long long teams = min((long long)a.teams, total);
+    auto bound = [&](long long k) { return total * k / teams; };
+    const long long s = team < teams ? bound(team) : total, e = team < teams ? bound(team + 1) : 0;
+    long long at = 0;  // where the sequences looked at next begin
+    int j = 0;
+    bool ok = true;
+    int2 cut = make_int2(-1, 0);
+    auto publish = [&](int b, long long begin, int w) {  // uniform over the warp
+      ok = ok && !*abort_flag;
+      if (ok && j >= C::ITEMS) ok = mbar_wait(&item_free[j % C::ITEMS], ((j / C::ITEMS) - 1) & 1, a.err);
+      if (!__all_sync(FULL, ok)) {
+        ok = false;
+        return;
+      }
+      LatentItem& d = items[j % C::ITEMS];
+      if (lane == 0) {
+        d.b = b;
+        if (b >= 0) {
+          const int L = latent_len(a, b);
+          int first, n;
+          latent_tiles(a, L, first, n);
+          const int t0 = (int)(max(s, begin) - begin), t1 = (int)(min(e, begin + w) - begin);
+          d.L = L;
+          d.first = first + t0;
+          d.n = n == 0 ? 0 : t1 - t0;
+          const bool whole = t0 == 0 && t1 == w;
+          // a team's range holds at most one cut piece that ends in it (its
+          // first) and one that goes on behind it (its last)
+          d.part = whole ? -1 : (team * a.row_tiles + rt) * 2 + (begin + w > e ? 1 : 0);
+          if (t0 == 0 && !whole) {  // the team of the sequence's last tile
+            long long k = (begin + w - 1) * teams / total;
+            while (bound(k + 1) <= begin + w - 1) ++k;
+            while (bound(k) > begin + w - 1) --k;
+            cut = make_int2(b, (int)k);
+          }
+          const int R0 = rt * NT, R1 = min(a.M, R0 + NT) - 1;
+          latent_visible(a, L, R0 / a.H, d.lo_u, d.hi_x);
+          latent_visible(a, L, R1 / a.H, d.lo_x, d.hi_u);
+        }
+      }
+      __syncwarp();
+      mbar_arrive(&item_full[j % C::ITEMS]);
+      if (!FP8 && b >= 0) {  // Q rows by TMA, once the item before has been multiplied
+        if (j >= 1) ok = mbar_wait(q_free, (j - 1) & 1, a.err);
+        ok = __all_sync(FULL, ok);
+        if (ok && lane == 0) {
+          mbar_arrive_expect_tx(q_full, C::Q_BYTES);
+#pragma unroll
+          for (int c = 0; c <= R / 64; ++c)
+            tma_load_2d(sbase + C::OFF_Q + c * (NT * 128), &map_q, c * 64, b * a.M + rt * NT, q_full);
+        }
+      }
+      ++j;
+    };
+    for (int w = 0; w < C::WARPS && ok && at < e; ++w) {
+      if (at + sums[w] <= s) {
+        at += sums[w];
+        continue;
+      }
+      const int b1 = min(a.B, (w + 1) * chunk);
+      for (int b0 = w * chunk; b0 < b1 && ok && at < e; b0 += 32) {
+        const int wt = b0 + lane < b1 ? latent_weight(a, b0 + lane) : 0;
+        int inc = wt;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(FULL, inc, o);
+          if (lane >= o) inc += y;
+        }
+        const long long begin = at + inc - wt;
+        unsigned hit = __ballot_sync(FULL, wt > 0 && begin < e && begin + wt > s);
+        while (hit && ok) {
+          const int src = __ffs(hit) - 1;
+          hit &= hit - 1;
+          publish(b0 + src, __shfl_sync(FULL, begin, src), __shfl_sync(FULL, wt, src));
+        }
+        at += __shfl_sync(FULL, inc, 31);
+      }
+    }
+    if (ok) publish(-1, 0, 0);
+    if (!ok) *abort_flag = 1;
+    if (rt == 0 && lane == 0) a.cut[team] = cut;
+    __syncwarp();
+  } else if (warp == 0) {
+    // ======================= TMA producer (whole warp) =========================
+    // Lane g copies page segment g of a tile. Block k of tile t (counted over
+    // all items) goes to slot (t * NB + k) % SLOTS.
+    if (lane == 0) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(&map_c) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(&map_r) : "memory");
+    }
+    const int seg_rows = min(a.page_size, kTile);
+    int g = 0, blk = 0;
+    bool ok = true;
+    for (int j = 0; ok; ++j) {
+      ok = __all_sync(FULL, !*abort_flag && mbar_wait(&item_full[j % C::ITEMS], (j / C::ITEMS) & 1, a.err));
+      if (!ok) break;
+      const LatentItem d = items[j % C::ITEMS];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&item_free[j % C::ITEMS]);
+      if (d.b < 0) break;
+      const int32_t* pt = a.page_table + (long long)d.b * a.max_pages;
+      const int pages = (d.L + a.page_size - 1) >> a.log2_page;
+      auto segments = [&](int t) {
+        return a.page_size >= kTile ? 1 : min(kTile >> a.log2_page, pages - ((t * kTile) >> a.log2_page));
+      };
+      auto page_of = [&](int t) -> int {  // this lane's page of tile t
+        if (t >= d.first + d.n || lane >= segments(t)) return 0;
+        return __ldg(pt + ((t * kTile) >> a.log2_page) + lane);
+      };
+      int pid = page_of(d.first), pid_next = page_of(d.first + 1);
+      for (int t = d.first; ok && t < d.first + d.n; ++t, ++g) {
+        const int nseg = segments(t);
+        if ((unsigned)pid >= (unsigned)a.num_pages) {
+          record_error_at(a.err, kErrBadPage);
+          pid = 0;
+        }
+        const int row = pid * a.page_size + (a.page_size >= kTile ? (t * kTile) & (a.page_size - 1) : 0);
+        const uint32_t off = (uint32_t)lane * seg_rows * 128u;
+        const uint32_t bytes = (uint32_t)(nseg * seg_rows) * 128u;
+        pid = pid_next;
+        pid_next = page_of(t + 2);
+#pragma unroll 1
+        for (int k = 0; k < C::NB; ++k, ++blk) {
+          const int sl = blk % C::SLOTS;
+          ok = !*abort_flag;
+          if (ok && blk >= C::SLOTS) ok = mbar_wait(&empty[sl], ((blk / C::SLOTS) - 1) & 1, a.err);
+          ok = __all_sync(FULL, ok);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&full[sl], FP8 ? bytes : 2 * bytes);
+          __syncwarp();
+          if (lane < nseg) {
+            const uint32_t dst = sbase + C::OFF_BLK + sl * C::BLK + off;
+            tma_load_2d(dst, &map_c, k * 128, row, &full[sl]);
+            if constexpr (!FP8) tma_load_2d(dst + C::HALF, &map_c, k * 128 + 64, row, &full[sl]);
+          }
+        }
+        if (!ok) break;
+        const int rs = g % C::R_SLOTS;
+        ok = !*abort_flag;
+        if (ok && g >= C::R_SLOTS) ok = mbar_wait(&rempty[rs], ((g / C::R_SLOTS) - 1) & 1, a.err);
+        ok = __all_sync(FULL, ok);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&rfull[rs], bytes);
+        __syncwarp();
+        if (lane < nseg) tma_load_2d(sbase + C::OFF_ROPE + rs * C::ROPE_SLOT + off, &map_r, 0, row, &rfull[rs]);
+      }
+    }
+    if (!ok) {
+      if (lane == 0) {
+        *abort_flag = 1;
+        // copies already issued land before the CTA's shared memory goes away
+        for (int n = max(0, blk - C::SLOTS); n < blk; ++n)
+          mbar_wait(&full[n % C::SLOTS], (n / C::SLOTS) & 1, a.err, kWaitTimeoutCycles / 16);
+        for (int n = max(0, g - C::R_SLOTS); n < g; ++n)
+          mbar_wait(&rfull[n % C::R_SLOTS], (n / C::R_SLOTS) & 1, a.err, kWaitTimeoutCycles / 16);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1 || warp == 2) {
+    // ======================= MMA issuers: S^T (warp 1), O^T (warp 2) ===========
+    if (lane == 0) {
+      bool ok = true;
+      int g = 0, blk = 0, issued = 0;
+      for (int j = 0; ok; ++j) {
+        ok = !*abort_flag && mbar_wait(&item_full[j % C::ITEMS], (j / C::ITEMS) & 1, a.err);
+        if (!ok) break;
+        const int n = items[j % C::ITEMS].n, b = items[j % C::ITEMS].b;
+        mbar_arrive(&item_free[j % C::ITEMS]);
+        if (b < 0) break;
+        if (warp == 1) {
+          ok = mbar_wait(q_full, j & 1, a.err);
+          for (int t = 0; ok && t < n; ++t, ++g) {
+            const int bb = g & 1;
+            if (g >= 2) ok = !*abort_flag && mbar_wait(&p_ready[bb], ((g - 2) >> 1) & 1, a.err);
+            const uint32_t dt = tmem + C::COL_S + bb * C::SN;
+            const uint32_t qa = sbase + C::OFF_Q;
+            for (int k = 0; ok && k < C::NB; ++k, ++blk) {
+              const int sl = blk % C::SLOTS;
+              ok = !*abort_flag && mbar_wait(&full[sl], (blk / C::SLOTS) & 1, a.err);
+              if (!ok) break;
+              tmem_fence_after();
+              const uint32_t ca = sbase + C::OFF_BLK + sl * C::BLK, qb = qa + k * C::Q_BLK;
+              if constexpr (FP8) {
+                constexpr uint32_t idesc = umma_idesc_e4m3(128, C::N1);
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                  umma_f8(dt, umma_desc(ca + s * 32, 16, 1024, kSw128),
+                          umma_desc(qb + s * 32, 16, 1024, kSw128), idesc, k > 0 || s > 0);
+              } else {
+                constexpr uint32_t idesc = umma_idesc_bf16(128, NT, false, false);
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                  umma_f16(dt, umma_desc(ca + (s >> 2) * C::HALF + (s & 3) * 32, 16, 1024, kSw128),
+                           umma_desc(qb + (s >> 2) * (NT * 128) + (s & 3) * 32, 16, 1024, kSw128),
+                           idesc, k > 0 || s > 0);
+              }
+            }
+            const int rs = g % C::R_SLOTS;
+            ok = ok && !*abort_flag && mbar_wait(&rfull[rs], (g / C::R_SLOTS) & 1, a.err);
+            if (!ok) break;
+            tmem_fence_after();
+            {
+              constexpr uint32_t idesc = umma_idesc_bf16(128, NT, false, false);
+              const uint32_t ra = sbase + C::OFF_ROPE + rs * C::ROPE_SLOT, qb = qa + C::Q_ROPE;
+#pragma unroll
+              for (int s = 0; s < 4; ++s)
+                umma_f16(FP8 ? dt + C::N1 : dt, umma_desc(ra + s * 32, 16, 1024, kSw128),
+                         umma_desc(qb + s * 32, 16, 1024, kSw128), idesc, !FP8 || s > 0);
+            }
+            if constexpr (!C::OVERLAY) umma_commit(&rempty[rs]);
+            umma_commit(&s_full[bb]);
+            issued = g + 1;
+          }
+          if (ok) umma_commit(q_free);
+        } else {
+          if (j >= 1) ok = mbar_wait(o_free, (j - 1) & 1, a.err);
+          for (int t = 0; ok && t < n; ++t, ++g) {
+            const int bb = g & 1;
+            ok = !*abort_flag && mbar_wait(&p_ready[bb], (g >> 1) & 1, a.err);
+            if (!ok) break;
+            tmem_fence_after();
+            const uint32_t pa = sbase + C::OFF_P + (g % C::P_BUFS) * C::P_BYTES;
+            constexpr uint32_t SBO = 8 * C::P_ROW;
+#pragma unroll 1
+            for (int k = 0; k < C::NB; ++k, ++blk) {
+              const int sl = blk % C::SLOTS;
+              const uint32_t ca = sbase + C::OFF_BLK + sl * C::BLK;
+              const uint32_t dt = tmem + C::COL_O + k * C::N2;
+              if constexpr (FP8) {
+                constexpr uint32_t idesc = umma_idesc_e4m3_mn(128, C::N2);
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                  umma_f8(dt, umma_desc(ca + s * 4096, C::HALF, 1024, kSw128),
+                          umma_desc(pa + s * 4 * SBO, C::P_BYTES, SBO, C::P_SWIZZLE), idesc, t > 0 || s > 0);
+              } else {
+                constexpr uint32_t idesc = umma_idesc_bf16(128, C::N2, true, true);
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                  umma_f16(dt, umma_desc(ca + s * 2048, C::HALF, 1024, kSw128),
+                           umma_desc(pa + s * 2 * SBO, C::P_BYTES, SBO, C::P_SWIZZLE), idesc, t > 0 || s > 0);
+              }
+              umma_commit(&empty[sl]);
+            }
+            if constexpr (C::OVERLAY) umma_commit(&rempty[g % C::R_SLOTS]);
+            umma_commit(&o_full[bb]);
+            issued = g + 1;
+          }
+        }
+      }
+      if (!ok) *abort_flag = 1;
+      if (*abort_flag && issued > 0) {  // MMAs already issued finish before TMEM is freed
+        uint64_t* last = warp == 1 ? &s_full[(issued - 1) & 1] : &o_full[(issued - 1) & 1];
+        mbar_wait(last, ((issued - 1) >> 1) & 1, a.err, kWaitTimeoutCycles / 16);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ======================= softmax ===========================================
+    // A group of four warps owns 16 query rows; thread i is token i of the tile
+    // in S^T and element i of each block in O^T.
+    constexpr int GT = 128;
+    constexpr float kLn2 = 0.69314718055994531f, kUnset = -1e30f;
+    const int q4 = warp & 3, grp = (warp - C::SOFT) >> 2, gbar = 2 + grp, r0 = 16 * grp;
+    const int i = 32 * q4 + lane;
+    const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
+    float* sm_m = reinterpret_cast<float*>(smem + C::OFF_M);
+    float* sm_alpha = reinterpret_cast<float*>(smem + C::OFF_ALPHA);
+    float* wmax = reinterpret_cast<float*>(smem + C::OFF_WMAX);
+    float* lred = reinterpret_cast<float*>(smem + C::OFF_LRED);
+    float* sm_inv = reinterpret_cast<float*>(smem + C::OFF_INV);
+    float* sm_cs = reinterpret_cast<float*>(smem + C::OFF_CS);
+    int2* sm_range = reinterpret_cast<int2*>(smem + C::OFF_RANGE);
+    const uint32_t s_tm = tmem + lane_off + C::COL_S + (FP8 ? 2 * r0 : r0);
+    const uint32_t o_tm = tmem + lane_off + C::COL_O + (FP8 ? 2 * r0 : r0);
+    int g = 0;
+    bool ok = true;
+    for (int j = 0; ok; ++j) {
+      const bool got = !*abort_flag && mbar_wait(&item_full[j % C::ITEMS], (j / C::ITEMS) & 1, a.err);
+      if (!named_bar_and(gbar, GT, got)) {
+        ok = false;
+        break;
+      }
+      const LatentItem& d = items[j % C::ITEMS];
+      if (d.b < 0) break;
+      const int first = d.first, n = d.n, L = d.L, b = d.b;
+      const int R0 = rt * NT + r0;  // this group's first packed row
+      if (i < 16) {
+        int lo = 0, hi = 0;
+        if (R0 + i < a.M) latent_visible(a, L, (R0 + i) / a.H, lo, hi);
+        sm_range[r0 + i] = make_int2(lo, hi);
+        sm_m[r0 + i] = kUnset;
+      }
+      if constexpr (FP8) {
+        // The item's Q operand. 2^e2 puts a row's max |q_c| in [128, 256); then
+        // q_c * 2^e2 = hi + lo / 16 in e4m3, exact for every element within
+        // 2^13 of the row's largest (others to 2^-21 of it).
+        if (j >= 1 && !mbar_wait(q_free, (j - 1) & 1, a.err)) *abort_flag = 1;
+        uint8_t* qs = smem + C::OFF_Q;
+        constexpr int E = R / 32;  // elements of a row per lane
+#pragma unroll 1
+        for (int rr = q4; rr < 16; rr += 4) {
+          const int nrow = r0 + rr, row = rt * NT + nrow;
+          float f[E];
+          uint4 rope = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int k = 0; k < E; ++k) f[k] = 0.f;
+          if (row < a.M) {
+            const uint16_t* src = a.q + ((long long)b * a.M + row) * (R + a.rope_dim);
+#pragma unroll
+            for (int k = 0; k < E / 8; ++k)
+              bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(src + lane * E + 8 * k)),
+                            *reinterpret_cast<float(*)[8]>(f + 8 * k));
+            if (lane * 8 < a.rope_dim) rope = __ldg(reinterpret_cast<const uint4*>(src + R + lane * 8));
+          }
+          float mx = 0.f;
+#pragma unroll
+          for (int k = 0; k < E; ++k) mx = fmaxf(mx, fabsf(f[k]));
+          mx = redux_max(mx);
+          const int e2 = mx > 0.f && mx < INFINITY ? min(7 - ilogbf(mx), 120) : 0;
+          const float up = ldexpf(1.f, e2);
+          if (lane == 0) sm_cs[nrow] = ldexpf(a.scale_log2, -e2);
+          uint32_t hw[E / 4], lw[E / 4];
+#pragma unroll
+          for (int w = 0; w < E / 4; ++w) {
+            hw[w] = lw[w] = 0;
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {
+              const float x0 = f[4 * w + k] * up, x1 = f[4 * w + k + 1] * up;
+              const uint32_t h2 = f32x2_to_e4m3x2(x0, x1);
+              hw[w] |= h2 << (8 * k);
+              lw[w] |= f32x2_to_e4m3x2((x0 - e4m3_to_f32(h2)) * 16.f, (x1 - e4m3_to_f32(h2 >> 8)) * 16.f) << (8 * k);
+            }
+          }
+          const int rh = 2 * r0 + rr, rl = rh + 16, el = lane * E;
+          uint8_t* blk_base = qs + (el >> 7) * C::Q_BLK;
+          const int c = (el & 127) >> 4;
+          if constexpr (E == 16) {
+            *reinterpret_cast<uint4*>(blk_base + sw128(rh, c)) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+            *reinterpret_cast<uint4*>(blk_base + sw128(rl, c)) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+          } else {
+            *reinterpret_cast<uint2*>(blk_base + sw128(rh, c) + (el & 8)) = make_uint2(hw[0], hw[1]);
+            *reinterpret_cast<uint2*>(blk_base + sw128(rl, c) + (el & 8)) = make_uint2(lw[0], lw[1]);
+          }
+          if (lane < 8) *reinterpret_cast<uint4*>(qs + C::Q_ROPE + sw128(nrow, lane)) = rope;
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(q_full);
+      }
+      named_bar(gbar, GT);
+      // FP8: this token's scale exponent, looked up a tile ahead
+      const int32_t* pt = a.page_table + (long long)b * a.max_pages;
+      auto scale_of = [&](int t) -> int {
+        const int jt = t * kTile + i;
+        if (!FP8 || t >= first + n || jt >= L) return 127;
+        const int page = __ldg(pt + (jt >> a.log2_page));
+        if ((unsigned)page >= (unsigned)a.num_pages) return 127;
+        return __ldg(a.scales + (long long)page * a.page_size + (jt & (a.page_size - 1)));
+      };
+      int sc_next = scale_of(first);
+      float l_sum[16], l_rnd[16];  // this token's part of the row sums: of the weights, of the rounded ones
+#pragma unroll
+      for (int r = 0; r < 16; ++r) l_sum[r] = l_rnd[r] = 0.f;
+      for (int t = first; t < first + n; ++t, ++g) {
+        const int bb = g & 1;
+        const float e_tok = FP8 ? (float)(min(max(sc_next, 97), 157) - 127) : 0.f;
+        sc_next = scale_of(t + 1);
+        bool good = __all_sync(FULL, !*abort_flag && mbar_wait(&s_full[bb], (g >> 1) & 1, a.err));
+        float x[16];
+        if (good) {
+          tmem_fence_after();
+          const uint32_t ta = s_tm + bb * C::SN;
+          if constexpr (FP8) {
+            const float up = __int_as_float((int)(e_tok + 127.f) << 23);
+            float y[16];
+            tmem_ld16(ta, x);
+            tmem_ld16(ta + 16, y);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) x[r] = fmaf(y[r], 0.0625f, x[r]) * up * sm_cs[r0 + r];
+            tmem_ld16(tmem + lane_off + C::COL_S + bb * C::SN + C::N1 + r0, y);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) x[r] = fmaf(y[r], a.scale_log2, x[r]) + e_tok;
+          } else {
+            tmem_ld16(ta, x);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) x[r] *= a.scale_log2;
+          }
+        } else {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) x[r] = -INFINITY;
+        }
+        const int t0 = t * kTile, jt = t0 + i;
+        if (!(t0 >= d.lo_x && t0 + kTile <= d.hi_x)) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int2 v = sm_range[r0 + r];
+            if (!(jt >= v.x && jt < v.y)) x[r] = -INFINITY;
+          }
+          // A token that no row sees may hold NaN: its latents become zeros
+          // before they meet its zero weights. The groups share the blocks.
+          if (good && (jt < d.lo_u || jt >= d.hi_u)) {
+            for (int k = grp; k < C::NB; k += C::GROUPS) {
+              uint8_t* row = smem + C::OFF_BLK + ((g * C::NB + k) % C::SLOTS) * C::BLK + i * 128;
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                const int cc = (c + i) & 7;
+                *reinterpret_cast<uint4*>(row + cc * 16) = make_uint4(0, 0, 0, 0);
+                if constexpr (!FP8) *reinterpret_cast<uint4*>(row + C::HALF + cc * 16) = make_uint4(0, 0, 0, 0);
+              }
+            }
+          }
+        }
+        // The running maximum moves only when a score passes it by so much that
+        // a weight would pass 2^8; most tiles skip the exchange.
+        bool want = !good;
+#pragma unroll
+        for (int r = 0; r < 16; r += 4) {
+          const float4 m = reinterpret_cast<const float4*>(sm_m + r0)[r / 4];
+          want |= (x[r] - m.x > 8.f) | (x[r + 1] - m.y > 8.f) | (x[r + 2] - m.z > 8.f) | (x[r + 3] - m.w > 8.f);
+        }
+        if (named_bar_or(gbar, GT, want)) {
+          if (!named_bar_and(gbar, GT, good)) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const float wm = redux_max(x[r]);
+            if (lane == r) wmax[q4 * NT + r0 + r] = wm;
+          }
+          named_bar(gbar, GT);
+          if (i < 16) {
+            const int rr = r0 + i;
+            const float top = fmaxf(fmaxf(wmax[rr], wmax[NT + rr]), fmaxf(wmax[2 * NT + rr], wmax[3 * NT + rr]));
+            const float m_old = sm_m[rr], m_new = fmaxf(m_old, top - C::HEAD);
+            sm_alpha[rr] = fast_exp2(m_old - m_new);
+            sm_m[rr] = m_new;
+          }
+          named_bar(gbar, GT);
+          const float* al = sm_alpha + r0;
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            l_sum[r] *= al[r];
+            l_rnd[r] *= al[r];
+          }
+          if (t > first) {  // what the item's earlier tiles added moves along
+            good = __all_sync(FULL, mbar_wait(&o_full[(g - 1) & 1], ((g - 1) >> 1) & 1, a.err));
+            if (good) {
+              tmem_fence_after();
+#pragma unroll 1
+              for (int k = 0; k < C::NB * (FP8 ? 2 : 1); ++k) {
+                const uint32_t ta = o_tm + (FP8 ? (k >> 1) * C::N2 + (k & 1) * 16 : k * C::N2);
+                float o[16];
+                tmem_ld16(ta, o);
+#pragma unroll
+                for (int r = 0; r < 16; ++r) o[r] *= al[r];
+                tmem_st16(ta, o);
+              }
+              tmem_fence_before();
+            } else {
+              *abort_flag = 1;
+            }
+          }
+        }
+        const float down = FP8 ? __int_as_float((int)(127.f - e_tok) << 23) : 1.f;
+#pragma unroll
+        for (int r = 0; r < 16; r += 4) {
+          const float4 m = reinterpret_cast<const float4*>(sm_m + r0)[r / 4];
+          x[r] = fast_exp2(x[r] - m.x);
+          x[r + 1] = fast_exp2(x[r + 1] - m.y);
+          x[r + 2] = fast_exp2(x[r + 2] - m.z);
+          x[r + 3] = fast_exp2(x[r + 3] - m.w);
+        }
+        uint32_t w[8];
+        if constexpr (FP8) {
+#pragma unroll
+          for (int r = 0; r < 16; r += 4) {
+            const uint32_t s01 = e4m3_split2(x[r], x[r + 1]), s23 = e4m3_split2(x[r + 2], x[r + 3]);
+            w[r / 4] = __byte_perm(s01, s23, 0x5410);
+            w[4 + r / 4] = __byte_perm(s01, s23, 0x7632);
+          }
+#pragma unroll
+          for (int r = 0; r < 16; ++r) l_sum[r] = fmaf(x[r], down, l_sum[r]);
+        } else {
+#pragma unroll
+          for (int r = 0; r < 16; r += 2) {
+            w[r / 2] = pack_bf16x2(x[r], x[r + 1]);
+            l_sum[r] += x[r];
+            l_sum[r + 1] += x[r + 1];
+            l_rnd[r] += __uint_as_float(w[r / 2] << 16);
+            l_rnd[r + 1] += __uint_as_float(w[r / 2] & 0xFFFF0000u);
+          }
+        }
+        // The buffer's last reader: the O^T products P_BUFS tiles ago. (Overlay:
+        // the rotated parts of this tile were loaded after those, and read.)
+        if (!C::OVERLAY && g >= C::P_BUFS) {
+          const int u = g - C::P_BUFS;
+          if (!mbar_wait(&o_full[u & 1], (u >> 1) & 1, a.err)) *abort_flag = 1;
+        }
+        uint8_t* sp = smem + C::OFF_P + (g % C::P_BUFS) * C::P_BYTES + i * C::P_ROW;
+        const int z = C::P_ROW == 128 ? i & 7 : C::P_ROW == 64 ? (i >> 1) & 3 : (i >> 2) & 1;
+        *reinterpret_cast<uint4*>(sp + (((2 * grp) ^ z) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(sp + (((2 * grp + 1) ^ z) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+        fence_proxy_async_smem();
+        tmem_fence_before();
+        mbar_arrive(&p_ready[bb]);
+      }
+      if (!ok) break;
+      // ---- the item's end: normalise O^T and store it, or the partial results
+      bool good = true;
+      if (n > 0) good = mbar_wait(&o_full[(g - 1) & 1], ((g - 1) >> 1) & 1, a.err);
+      if (!named_bar_and(gbar, GT, good && !*abort_flag)) {
+        ok = false;
+        break;
+      }
+      tmem_fence_after();
+#pragma unroll 1
+      for (int what = 0; what < (FP8 ? 1 : 2); ++what) {  // sums over the 128 tokens, in one order
+        if (what == 1) named_bar(gbar, GT);               // the first sums have been read
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          float v = what == 0 ? l_sum[r] : l_rnd[r];
+#pragma unroll
+          for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
+          if (lane == 0) lred[q4 * NT + r0 + r] = v;
+        }
+        named_bar(gbar, GT);
+        if (i < 16) {
+          const int rr = r0 + i, row = rt * NT + rr;
+          const float l = lred[rr] + lred[NT + rr] + lred[2 * NT + rr] + lred[3 * NT + rr];
+          if (what == 0 && row < a.M) {
+            const float lse = l > 0.f ? (sm_m[rr] + log2f(l)) * kLn2 : -INFINITY;
+            if (d.part >= 0) a.lse_part[(long long)d.part * NT + rr] = lse;
+            else if (a.lse) a.lse[(long long)b * a.M + row] = lse;
+          }
+          if (FP8 || what == 1) sm_inv[rr] = l > 0.f ? 1.f / l : 0.f;
+        }
+      }
+      named_bar(gbar, GT);
+      const int part = d.part, rows = min(16, a.M - R0);
+#pragma unroll 1
+      for (int k = 0; k < C::NB; ++k) {
+        float o[16];
+        if (n > 0) {
+          tmem_ld16(o_tm + k * C::N2, o);
+          if constexpr (FP8) {
+            float lo[16];
+            tmem_ld16(o_tm + k * C::N2 + 16, lo);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) o[r] = fmaf(lo[r], 0.0625f, o[r]);
+          }
+        } else {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) o[r] = 0.f;
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          if (r < rows) {
+            const float inv = sm_inv[r0 + r], v = inv > 0.f ? o[r] * inv : 0.f;
+            if (part >= 0)
+              a.o_part[((long long)part * NT + r0 + r) * R + k * 128 + i] = v;
+            else
+              a.out[((long long)b * a.M + R0 + r) * R + k * 128 + i] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+          }
+        }
+      }
+      tmem_fence_before();
+      mbar_arrive(o_free);
+      named_bar(gbar, GT);  // the group no longer reads the item and its row state
+      if (i == 0) mbar_arrive(&item_free[j % C::ITEMS]);
+    }
+    if (!ok) *abort_flag = 1;
+  }
+
+  pdl_launch_dependents();
+  tmem_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tmem_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS)
+                 : "memory");
+  }
+}
+
+// Joins the partial results of the sequences that lie in several teams' ranges:
+// lse = ln sum_k exp(lse_k), out = sum_k exp(lse_k - lse) o_k. Block (team, y)
+// takes the cut sequence that starts in the team's range, rows y, y + gridDim.y,
+// ...; its threads are 4 groups of parts x R / 4 columns of four elements.
+template <int R>
+__global__ void __launch_bounds__(R) latent_merge_kernel(const LatentArgs a, int nt) {
+  constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
+  constexpr int CT = R / 4;
+  __shared__ float4 part_o[3][CT];
+  pdl_wait_primary();
+  const int team = blockIdx.x, tid = threadIdx.x, grp = tid / CT, col = tid % CT;
+  const int2 cut = a.cut[team];
+  if (cut.x < 0) return;
+  const int parts = cut.y - team + 1;
+  for (int row = blockIdx.y; row < a.M; row += gridDim.y) {
+    const int rt = row / nt, rr = row - rt * nt;
+    // slot of part k: the piece goes on behind the team's range but in the last
+    auto slot = [&](int k) {
+      return ((long long)((team + k) * a.row_tiles + rt) * 2 + (k + 1 < parts ? 1 : 0)) * nt + rr;
+    };
+    float m = -INFINITY;
+    for (int k = tid & 31; k < parts; k += 32) m = fmaxf(m, a.lse_part[slot(k)]);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    float sum = 0.f;
+    if (m != -INFINITY)
+      for (int k = tid & 31; k < parts; k += 32) sum += exp2f((a.lse_part[slot(k)] - m) * kLog2e);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    const float lse = m == -INFINITY ? -INFINITY : m + log2f(sum) * kLn2;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (m != -INFINITY) {
+#pragma unroll 4
+      for (int k = grp; k < parts; k += 4) {
+        const long long s = slot(k);
+        const float l = a.lse_part[s];
+        const float w = l == -INFINITY ? 0.f : exp2f((l - lse) * kLog2e);
+        const float4 v = *reinterpret_cast<const float4*>(a.o_part + s * R + col * 4);
+        acc.x = fmaf(w, v.x, acc.x);
+        acc.y = fmaf(w, v.y, acc.y);
+        acc.z = fmaf(w, v.z, acc.z);
+        acc.w = fmaf(w, v.w, acc.w);
+      }
+    }
+    if (grp > 0) part_o[grp - 1][col] = acc;
+    __syncthreads();
+    if (grp == 0) {
+#pragma unroll
+      for (int x = 0; x < 3; ++x) {
+        const float4 v = part_o[x][col];
+        acc.x += v.x;
+        acc.y += v.y;
+        acc.z += v.z;
+        acc.w += v.w;
+      }
+      const long long o = (long long)cut.x * a.M + row;
+      *reinterpret_cast<uint2*>(a.out + o * R + col * 4) =
+          make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+      if (col == 0 && a.lse) a.lse[o] = lse;
+    }
+    __syncthreads();
+  }
+}
+
+}  // namespace pda

@@ -66,6 +66,33 @@ pda_status device_state(DeviceState** out) {
   return PDA_OK;
 }
 
+// The library-owned workspace, made at least `bytes` large. Growing is
+// stream-ordered: the old buffer is released after the work already queued on
+// `stream`, the new one is ready for the work queued next, and neither step
+// synchronises the device. A call being captured into a CUDA graph cannot
+// grow the buffer (the allocation would belong to the graph).
+pda_status grow_library_workspace(DeviceState* dev, size_t bytes, cudaStream_t stream, void** out) {
+  std::lock_guard<std::mutex> lock(g_mu);
+  if (dev->ws_bytes >= bytes) {
+    *out = dev->ws;
+    return PDA_OK;
+  }
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) return PDA_ERR_CUDA;
+  if (cap != cudaStreamCaptureStatusNone) return PDA_ERR_WORKSPACE;
+  if (dev->ws && cudaFreeAsync(dev->ws, stream) != cudaSuccess) return PDA_ERR_CUDA;
+  dev->ws = nullptr;
+  dev->ws_bytes = 0;
+  void* fresh = nullptr;
+  if (cudaMallocAsync(&fresh, bytes, stream) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return PDA_ERR_WORKSPACE;
+  }
+  dev->ws = *out = fresh;
+  dev->ws_bytes = bytes;
+  return PDA_OK;
+}
+
 bool is_pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
 int ilog2(int x) { int l = 0; while ((1 << l) < x) ++l; return l; }
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -235,6 +262,23 @@ int* device_error_word() {
   return device_state(&st) == PDA_OK ? st->err : nullptr;
 }
 
+int device_sms() {
+  DeviceState* st = nullptr;
+  return device_state(&st) == PDA_OK ? st->num_sms : 0;
+}
+
+// The library-owned workspace, at least `bytes` large, for a call that is not
+// being captured (PDA_ERR_WORKSPACE otherwise).
+pda_status library_workspace(size_t bytes, cudaStream_t stream, void** out) {
+  DeviceState* dev = nullptr;
+  pda_status st = device_state(&dev);
+  if (st != PDA_OK) return st;
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) return PDA_ERR_CUDA;
+  if (cap != cudaStreamCaptureStatusNone) return PDA_ERR_WORKSPACE;
+  return grow_library_workspace(dev, bytes, stream, out);
+}
+
 cudaError_t launch_merge(int D, const float* o_parts, const float* lse_parts,
                          int num_splits, long long rows, float* out, float* lse,
                          const float* sinks, int Hq, cudaStream_t stream, bool pdl) {
@@ -373,28 +417,7 @@ pda_status paged_decode_attn(const void* q, const void* k_pages, const void* v_p
   if (wl.total > 0) {
     void* ws = p.workspace;
     if (ws == nullptr) {
-      std::lock_guard<std::mutex> lock(g_mu);
-      if (dev->ws_bytes < wl.total) {
-        // Grow stream-ordered: the old buffer is released after the work
-        // already queued on `stream`, the new one is ready for the work
-        // queued next, and neither step synchronises the device. A call
-        // being captured into a CUDA graph cannot grow the buffer (the
-        // allocation would belong to the graph).
-        cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-        if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) return PDA_ERR_CUDA;
-        if (cap != cudaStreamCaptureStatusNone) return PDA_ERR_WORKSPACE;
-        if (dev->ws && cudaFreeAsync(dev->ws, stream) != cudaSuccess) return PDA_ERR_CUDA;
-        dev->ws = nullptr;
-        dev->ws_bytes = 0;
-        void* fresh = nullptr;
-        if (cudaMallocAsync(&fresh, wl.total, stream) != cudaSuccess) {
-          (void)cudaGetLastError();
-          return PDA_ERR_WORKSPACE;
-        }
-        dev->ws = fresh;
-        dev->ws_bytes = wl.total;
-      }
-      ws = dev->ws;
+      if ((st = grow_library_workspace(dev, wl.total, stream, &ws)) != PDA_OK) return st;
     } else if (p.workspace_bytes < wl.total) {
       return PDA_ERR_WORKSPACE;
     }
