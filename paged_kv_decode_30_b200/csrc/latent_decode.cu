@@ -1,6 +1,7 @@
 // Latent decode attention, absorbed form: validation and launch.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -34,6 +35,8 @@ pda_status validate(const pda_latent_params* p) {
       p->page_size < 8 || p->page_size > 256 || (p->page_size & (p->page_size - 1)) ||
       p->kv_dtype == PDA_KV_NVFP4 || p->q_len > 8 || p->num_heads > 256 || p->batch > 65535)
     return PDA_ERR_UNSUPPORTED;
+  if (p->batch * (((long long)p->max_pages_per_seq * p->page_size + 127) / 128) > INT_MAX)
+    return PDA_ERR_UNSUPPORTED;  // tiles are counted in 32 bits
   return PDA_OK;
 }
 
@@ -54,7 +57,7 @@ Plan make_plan(const pda_latent_params& p, int sms) {
   // One CTA per SM; a team walks a range of tokens with a CTA per row tile.
   // Never more teams than tiles.
   const long long tiles = (long long)p.batch * (((long long)p.max_pages_per_seq * p.page_size + 127) / 128);
-  const long long teams = sms / pl.row_tiles;
+  const long long teams = std::min(sms, 512) / pl.row_tiles;  // 512: what the merge can list
   pl.teams = (int)(teams < 1 ? 1 : teams < tiles ? teams : tiles);
   const size_t slots = (size_t)pl.teams * pl.row_tiles * 2 * pl.nt;
   pl.lse_off = slots * p.latent_dim * sizeof(float);

@@ -126,7 +126,7 @@ struct LatentCfg {
   static constexpr int P_BUFS = (OVERLAY || (!FP8 && NT == 32 && R == 512)) ? 1 : 2;
   static constexpr int R_SLOTS = FP8 ? 2 : 1;
   static constexpr int ROPE_SLOT = HALF;
-  static constexpr int STATE = 16 * NT * 4 + 1024;
+  static constexpr int STATE = 20 * NT * 4 + 1024;
   static constexpr int FREE = 227 * 1024 - 1024 - STATE - Q_BYTES - (OVERLAY ? 0 : P_BUFS * P_BYTES) -
                               R_SLOTS * ROPE_SLOT;
   static constexpr int SLOTS = FREE / BLK < 3 * NB ? FREE / BLK : 3 * NB;
@@ -138,8 +138,8 @@ struct LatentCfg {
   static constexpr int OFF_M = OFF_STATE;               // running maximum per row
   static constexpr int OFF_ALPHA = OFF_M + NT * 4;
   static constexpr int OFF_WMAX = OFF_ALPHA + NT * 4;   // [4][NT]
-  static constexpr int OFF_LRED = OFF_WMAX + 4 * NT * 4;   // [4][NT]: also the rounded sums'
-  static constexpr int OFF_INV = OFF_LRED + 4 * NT * 4;
+  static constexpr int OFF_LRED = OFF_WMAX + 4 * NT * 4;   // [2][4][NT]: sums of weights, of rounded ones
+  static constexpr int OFF_INV = OFF_LRED + 8 * NT * 4;
   static constexpr int OFF_CS = OFF_INV + NT * 4;       // score scale per row (FP8)
   static constexpr int OFF_RANGE = OFF_CS + NT * 4;     // int2 visible keys per row
   static constexpr int OFF_ITEM = OFF_RANGE + NT * 8;
@@ -147,7 +147,7 @@ struct LatentCfg {
   static constexpr int OFF_BAR = OFF_ITEM + ITEMS * (int)sizeof(LatentItem);
   static constexpr int BARS = 2 * SLOTS + 2 * R_SLOTS + 2 + 2 + 2 + 3 + 2 * ITEMS;
   static constexpr int OFF_MISC = OFF_BAR + BARS * 8;   // TMEM address, abort flag, scan sums
-  static constexpr int SMEM = OFF_MISC + 16 + 32 * 8;
+  static constexpr int SMEM = OFF_MISC + 16 + 32 * 4;
   static constexpr int SMEM_ALLOC = SMEM + 1024;
   static constexpr int GROUPS = NT / 16;
   static constexpr int SOFT = 4;                        // first softmax warp
@@ -167,6 +167,28 @@ struct LatentCfg {
 // 128-byte-swizzled address of 16-byte piece c of row n in a block of rows.
 __device__ __forceinline__ uint32_t sw128(int n, int c) {
   return (n >> 3) * 1024 + (n & 7) * 128 + ((c ^ (n & 7)) << 4);
+}
+
+// One lane of a converged warp (the same one every time).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// Sums of 16 values over a warp's lanes: every step hands half of the values
+// to the partner, so lane l ends with the sum of value l / 2 in v[0].
+__device__ __forceinline__ void lane_sums(float (&v)[16], int lane) {
+#pragma unroll
+  for (int h = 8; h >= 1; h >>= 1) {
+    const bool up = lane & (2 * h);
+#pragma unroll
+    for (int k = 0; k < h; ++k) {
+      const float send = up ? v[k] : v[k + h], keep = up ? v[k + h] : v[k];
+      v[k] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, 2 * h);
+    }
+  }
+  v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], 1);
 }
 
 template <int R, bool FP8, int NT>
@@ -196,7 +218,7 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
   uint64_t* item_free = item_full + C::ITEMS;  // [ITEMS]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
-  long long* sums = reinterpret_cast<long long*>(smem + C::OFF_MISC + 16);  // [WARPS]
+  int* sums = reinterpret_cast<int*>(smem + C::OFF_MISC + 16);  // [WARPS]
   LatentItem* items = reinterpret_cast<LatentItem*>(smem + C::OFF_ITEM);
 
   if (tid == 0) {
@@ -233,36 +255,37 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
   // Each warp adds up one chunk of the sequences' weights.
   const int chunk = (a.B + C::WARPS - 1) / C::WARPS;
   {
-    long long w = 0;
+    int w = 0;  // (the host refuses calls of 2^31 tiles or more)
     for (int b = warp * chunk + lane; b < min(a.B, (warp + 1) * chunk); b += 32) {
       w += latent_weight(a, b);
       const int L = __ldg(a.kv_lens + b);
       if (blockIdx.x == 0 && (L < 0 || L > (a.max_pages << a.log2_page))) record_error_at(a.err, kErrBadPage);
     }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) w += __shfl_xor_sync(FULL, w, o);
+    w = __reduce_add_sync(FULL, w);
     if (lane == 0) sums[warp] = w;
   }
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_launch_dependents();  // the merge may be set up beside us; it waits for our end
 
   if (warp == 3) {
     // ======================= schedule (whole warp) =============================
     // The line's length and this team's range [s, e) of it (a line shorter than
     // the number of teams leaves the last ones idle, so that no range is empty);
     // then every sequence that overlaps the range becomes an item.
-    long long total = 0;
-    for (int w = 0; w < C::WARPS; ++w) total += sums[w];
-    const long long teams = min((long long)a.teams, total);
-    auto bound = [&](long long k) { return total * k / teams; };
-    const long long s = team < teams ? bound(team) : total, e = team < teams ? bound(team + 1) : 0;
-    long long at = 0;  // where the sequences looked at next begin
+    int total = lane < C::WARPS ? sums[lane] : 0;
+    total = __reduce_add_sync(FULL, total);
+    // the first `more` teams take share + 1 units, the rest share
+    const int teams = min(a.teams, total), share = total / teams, more = total - share * teams;
+    const int s = team < teams ? share * team + min(team, more) : total;
+    const int e = team < teams ? s + share + (team < more ? 1 : 0) : 0;
+    int at = 0;  // where the sequences looked at next begin
     int j = 0;
     bool ok = true;
     int2 cut = make_int2(-1, 0);
-    auto publish = [&](int b, long long begin, int w) {  // uniform over the warp
+    auto publish = [&](int b, int begin, int w) {  // uniform over the warp
       ok = ok && !*abort_flag;
       if (ok && j >= C::ITEMS) ok = mbar_wait(&item_free[j % C::ITEMS], ((j / C::ITEMS) - 1) & 1, a.err);
       if (!__all_sync(FULL, ok)) {
@@ -276,7 +299,7 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
           const int L = latent_len(a, b);
           int first, n;
           latent_tiles(a, L, first, n);
-          const int t0 = (int)(max(s, begin) - begin), t1 = (int)(min(e, begin + w) - begin);
+          const int t0 = max(s, begin) - begin, t1 = min(e, begin + w) - begin;
           d.L = L;
           d.first = first + t0;
           d.n = n == 0 ? 0 : t1 - t0;
@@ -285,10 +308,8 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
           // first) and one that goes on behind it (its last)
           d.part = whole ? -1 : (team * a.row_tiles + rt) * 2 + (begin + w > e ? 1 : 0);
           if (t0 == 0 && !whole) {  // the team of the sequence's last tile
-            long long k = (begin + w - 1) * teams / total;
-            while (bound(k + 1) <= begin + w - 1) ++k;
-            while (bound(k) > begin + w - 1) --k;
-            cut = make_int2(b, (int)k);
+            const int last = begin + w - 1, wide = (share + 1) * more;
+            cut = make_int2(b, last < wide ? last / (share + 1) : more + (last - wide) / share);
           }
           const int R0 = rt * NT, R1 = min(a.M, R0 + NT) - 1;
           latent_visible(a, L, R0 / a.H, d.lo_u, d.hi_x);
@@ -323,7 +344,7 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
           const int y = __shfl_up_sync(FULL, inc, o);
           if (lane >= o) inc += y;
         }
-        const long long begin = at + inc - wt;
+        const int begin = at + inc - wt;
         unsigned hit = __ballot_sync(FULL, wt > 0 && begin < e && begin + wt > s);
         while (hit && ok) {
           const int src = __ffs(hit) - 1;
@@ -415,100 +436,113 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
     __syncwarp();
   } else if (warp == 1 || warp == 2) {
     // ======================= MMA issuers: S^T (warp 1), O^T (warp 2) ===========
-    if (lane == 0) {
-      bool ok = true;
-      int g = 0, blk = 0, issued = 0;
-      for (int j = 0; ok; ++j) {
-        ok = !*abort_flag && mbar_wait(&item_full[j % C::ITEMS], (j / C::ITEMS) & 1, a.err);
-        if (!ok) break;
-        const int n = items[j % C::ITEMS].n, b = items[j % C::ITEMS].b;
-        mbar_arrive(&item_free[j % C::ITEMS]);
-        if (b < 0) break;
-        if (warp == 1) {
-          ok = mbar_wait(q_full, j & 1, a.err);
-          for (int t = 0; ok && t < n; ++t, ++g) {
-            const int bb = g & 1;
-            if (g >= 2) ok = !*abort_flag && mbar_wait(&p_ready[bb], ((g - 2) >> 1) & 1, a.err);
-            const uint32_t dt = tmem + C::COL_S + bb * C::SN;
-            const uint32_t qa = sbase + C::OFF_Q;
-            for (int k = 0; ok && k < C::NB; ++k, ++blk) {
-              const int sl = blk % C::SLOTS;
-              ok = !*abort_flag && mbar_wait(&full[sl], (blk / C::SLOTS) & 1, a.err);
-              if (!ok) break;
-              tmem_fence_after();
-              const uint32_t ca = sbase + C::OFF_BLK + sl * C::BLK, qb = qa + k * C::Q_BLK;
+    // The whole warp follows the loop and one elected lane issues: the
+    // operands then stay in uniform registers, and an MMA costs what the
+    // tensor core and its shared-memory reads take (measured: 48 cycles at 64
+    // columns, 40 at 32; from a single-lane branch 58 to 73). Descriptors of
+    // one operand differ by constants in their address field.
+    const bool leader = elect_one();
+    bool ok = true;
+    int g = 0, blk = 0, issued = 0;
+    auto agreed = [&](bool v) { return __all_sync(FULL, v); };
+    for (int j = 0; ok; ++j) {
+      ok = agreed(!*abort_flag && mbar_wait(&item_full[j % C::ITEMS], (j / C::ITEMS) & 1, a.err));
+      if (!ok) break;
+      const int n = items[j % C::ITEMS].n, b = items[j % C::ITEMS].b;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&item_free[j % C::ITEMS]);
+      if (b < 0) break;
+      if (warp == 1) {
+        ok = agreed(mbar_wait(q_full, j & 1, a.err));
+        for (int t = 0; ok && t < n; ++t, ++g) {
+          const int bb = g & 1;
+          if (g >= 2) ok = agreed(!*abort_flag && mbar_wait(&p_ready[bb], ((g - 2) >> 1) & 1, a.err));
+          const uint32_t dt = tmem + C::COL_S + bb * C::SN;
+          const uint64_t q0 = umma_desc(sbase + C::OFF_Q, 16, 1024, kSw128);
+#pragma unroll 1
+          for (int k = 0; ok && k < C::NB; ++k, ++blk) {
+            const int sl = blk % C::SLOTS;
+            ok = agreed(!*abort_flag && mbar_wait(&full[sl], (blk / C::SLOTS) & 1, a.err));
+            if (!ok) break;
+            tmem_fence_after();
+            const uint64_t ca = umma_desc(sbase + C::OFF_BLK + sl * C::BLK, 16, 1024, kSw128);
+            const uint64_t qb = q0 + ((k * C::Q_BLK) >> 4);
+            if (leader) {
               if constexpr (FP8) {
                 constexpr uint32_t idesc = umma_idesc_e4m3(128, C::N1);
 #pragma unroll
-                for (int s = 0; s < 4; ++s)
-                  umma_f8(dt, umma_desc(ca + s * 32, 16, 1024, kSw128),
-                          umma_desc(qb + s * 32, 16, 1024, kSw128), idesc, k > 0 || s > 0);
+                for (int s = 0; s < 4; ++s) umma_f8(dt, ca + 2 * s, qb + 2 * s, idesc, k > 0 || s > 0);
               } else {
                 constexpr uint32_t idesc = umma_idesc_bf16(128, NT, false, false);
 #pragma unroll
                 for (int s = 0; s < 8; ++s)
-                  umma_f16(dt, umma_desc(ca + (s >> 2) * C::HALF + (s & 3) * 32, 16, 1024, kSw128),
-                           umma_desc(qb + (s >> 2) * (NT * 128) + (s & 3) * 32, 16, 1024, kSw128),
-                           idesc, k > 0 || s > 0);
+                  umma_f16(dt, ca + (((s >> 2) * C::HALF + (s & 3) * 32) >> 4),
+                           qb + (((s >> 2) * (NT * 128) + (s & 3) * 32) >> 4), idesc, k > 0 || s > 0);
               }
             }
-            const int rs = g % C::R_SLOTS;
-            ok = ok && !*abort_flag && mbar_wait(&rfull[rs], (g / C::R_SLOTS) & 1, a.err);
-            if (!ok) break;
-            tmem_fence_after();
-            {
-              constexpr uint32_t idesc = umma_idesc_bf16(128, NT, false, false);
-              const uint32_t ra = sbase + C::OFF_ROPE + rs * C::ROPE_SLOT, qb = qa + C::Q_ROPE;
+            __syncwarp();
+          }
+          const int rs = g % C::R_SLOTS;
+          ok = agreed(ok && !*abort_flag && mbar_wait(&rfull[rs], (g / C::R_SLOTS) & 1, a.err));
+          if (!ok) break;
+          tmem_fence_after();
+          if (leader) {
+            constexpr uint32_t idesc = umma_idesc_bf16(128, NT, false, false);
+            const uint64_t ra = umma_desc(sbase + C::OFF_ROPE + rs * C::ROPE_SLOT, 16, 1024, kSw128);
+            const uint64_t qb = q0 + (C::Q_ROPE >> 4);
 #pragma unroll
-              for (int s = 0; s < 4; ++s)
-                umma_f16(FP8 ? dt + C::N1 : dt, umma_desc(ra + s * 32, 16, 1024, kSw128),
-                         umma_desc(qb + s * 32, 16, 1024, kSw128), idesc, !FP8 || s > 0);
-            }
+            for (int s = 0; s < 4; ++s)
+              umma_f16(FP8 ? dt + C::N1 : dt, ra + 2 * s, qb + 2 * s, idesc, !FP8 || s > 0);
             if constexpr (!C::OVERLAY) umma_commit(&rempty[rs]);
             umma_commit(&s_full[bb]);
-            issued = g + 1;
           }
-          if (ok) umma_commit(q_free);
-        } else {
-          if (j >= 1) ok = mbar_wait(o_free, (j - 1) & 1, a.err);
-          for (int t = 0; ok && t < n; ++t, ++g) {
-            const int bb = g & 1;
-            ok = !*abort_flag && mbar_wait(&p_ready[bb], (g >> 1) & 1, a.err);
-            if (!ok) break;
-            tmem_fence_after();
-            const uint32_t pa = sbase + C::OFF_P + (g % C::P_BUFS) * C::P_BYTES;
-            constexpr uint32_t SBO = 8 * C::P_ROW;
+          __syncwarp();
+          issued = g + 1;
+        }
+        if (ok && leader) umma_commit(q_free);
+      } else {
+        if (j >= 1) ok = agreed(mbar_wait(o_free, (j - 1) & 1, a.err));
+        for (int t = 0; ok && t < n; ++t, ++g) {
+          const int bb = g & 1;
+          ok = agreed(!*abort_flag && mbar_wait(&p_ready[bb], (g >> 1) & 1, a.err));
+          if (!ok) break;
+          tmem_fence_after();
+          constexpr uint32_t SBO = 8 * C::P_ROW;
+          const uint64_t pd = umma_desc(sbase + C::OFF_P + (g % C::P_BUFS) * C::P_BYTES, C::P_BYTES, SBO, C::P_SWIZZLE);
 #pragma unroll 1
-            for (int k = 0; k < C::NB; ++k, ++blk) {
-              const int sl = blk % C::SLOTS;
-              const uint32_t ca = sbase + C::OFF_BLK + sl * C::BLK;
-              const uint32_t dt = tmem + C::COL_O + k * C::N2;
+          for (int k = 0; k < C::NB; ++k, ++blk) {
+            const int sl = blk % C::SLOTS;
+            const uint64_t ca = umma_desc(sbase + C::OFF_BLK + sl * C::BLK, C::HALF, 1024, kSw128);
+            const uint32_t dt = tmem + C::COL_O + k * C::N2;
+            if (leader) {
               if constexpr (FP8) {
                 constexpr uint32_t idesc = umma_idesc_e4m3_mn(128, C::N2);
 #pragma unroll
                 for (int s = 0; s < 4; ++s)
-                  umma_f8(dt, umma_desc(ca + s * 4096, C::HALF, 1024, kSw128),
-                          umma_desc(pa + s * 4 * SBO, C::P_BYTES, SBO, C::P_SWIZZLE), idesc, t > 0 || s > 0);
+                  umma_f8(dt, ca + ((s * 4096) >> 4), pd + ((s * 4 * SBO) >> 4), idesc, t > 0 || s > 0);
               } else {
                 constexpr uint32_t idesc = umma_idesc_bf16(128, C::N2, true, true);
 #pragma unroll
                 for (int s = 0; s < 8; ++s)
-                  umma_f16(dt, umma_desc(ca + s * 2048, C::HALF, 1024, kSw128),
-                           umma_desc(pa + s * 2 * SBO, C::P_BYTES, SBO, C::P_SWIZZLE), idesc, t > 0 || s > 0);
+                  umma_f16(dt, ca + ((s * 2048) >> 4), pd + ((s * 2 * SBO) >> 4), idesc, t > 0 || s > 0);
               }
               umma_commit(&empty[sl]);
             }
+            __syncwarp();
+          }
+          if (leader) {
             if constexpr (C::OVERLAY) umma_commit(&rempty[g % C::R_SLOTS]);
             umma_commit(&o_full[bb]);
-            issued = g + 1;
           }
+          __syncwarp();
+          issued = g + 1;
         }
       }
-      if (!ok) *abort_flag = 1;
-      if (*abort_flag && issued > 0) {  // MMAs already issued finish before TMEM is freed
-        uint64_t* last = warp == 1 ? &s_full[(issued - 1) & 1] : &o_full[(issued - 1) & 1];
-        mbar_wait(last, ((issued - 1) >> 1) & 1, a.err, kWaitTimeoutCycles / 16);
-      }
+    }
+    if (!ok) *abort_flag = 1;
+    if (*abort_flag && issued > 0) {  // MMAs already issued finish before TMEM is freed
+      uint64_t* last = warp == 1 ? &s_full[(issued - 1) & 1] : &o_full[(issued - 1) & 1];
+      mbar_wait(last, ((issued - 1) >> 1) & 1, a.err, kWaitTimeoutCycles / 16);
     }
     __syncwarp();
   } else {
@@ -770,32 +804,35 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
         break;
       }
       tmem_fence_after();
-#pragma unroll 1
-      for (int what = 0; what < (FP8 ? 1 : 2); ++what) {  // sums over the 128 tokens, in one order
-        if (what == 1) named_bar(gbar, GT);               // the first sums have been read
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          float v = what == 0 ? l_sum[r] : l_rnd[r];
-#pragma unroll
-          for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
-          if (lane == 0) lred[q4 * NT + r0 + r] = v;
-        }
-        named_bar(gbar, GT);
-        if (i < 16) {
-          const int rr = r0 + i, row = rt * NT + rr;
-          const float l = lred[rr] + lred[NT + rr] + lred[2 * NT + rr] + lred[3 * NT + rr];
-          if (what == 0 && row < a.M) {
-            const float lse = l > 0.f ? (sm_m[rr] + log2f(l)) * kLn2 : -INFINITY;
-            if (d.part >= 0) a.lse_part[(long long)d.part * NT + rr] = lse;
-            else if (a.lse) a.lse[(long long)b * a.M + row] = lse;
-          }
-          if (FP8 || what == 1) sm_inv[rr] = l > 0.f ? 1.f / l : 0.f;
-        }
+      // sums over the 128 tokens, in one order: over the warp's lanes, each
+      // lane ending with one row's sum, then over the four warps
+      lane_sums(l_sum, lane);
+      if constexpr (!FP8) lane_sums(l_rnd, lane);
+      if ((lane & 1) == 0) {
+        lred[q4 * NT + r0 + (lane >> 1)] = l_sum[0];
+        if constexpr (!FP8) lred[(4 + q4) * NT + r0 + (lane >> 1)] = l_rnd[0];
       }
       named_bar(gbar, GT);
       const int part = d.part, rows = min(16, a.M - R0);
+      if (i < 16) {
+        const int rr = r0 + i;
+        const float l = lred[rr] + lred[NT + rr] + lred[2 * NT + rr] + lred[3 * NT + rr];
+        const float ln = FP8 ? l : lred[4 * NT + rr] + lred[5 * NT + rr] + lred[6 * NT + rr] + lred[7 * NT + rr];
+        if (i < rows) {
+          const float lse = l > 0.f ? (sm_m[rr] + log2f(l)) * kLn2 : -INFINITY;
+          if (part >= 0) a.lse_part[(long long)part * NT + rr] = lse;
+          else if (a.lse) a.lse[(long long)b * a.M + R0 + i] = lse;
+        }
+        sm_inv[rr] = ln > 0.f ? 1.f / ln : 0.f;
+      }
+      named_bar(gbar, GT);
+      float inv[16];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) inv[r] = sm_inv[r0 + r];
+      float* po = a.o_part + ((long long)part * NT + r0) * R + i;
+      uint16_t* oo = a.out + ((long long)b * a.M + R0) * R + i;
 #pragma unroll 1
-      for (int k = 0; k < C::NB; ++k) {
+      for (int k = 0; k < C::NB; ++k, po += 128, oo += 128) {
         float o[16];
         if (n > 0) {
           tmem_ld16(o_tm + k * C::N2, o);
@@ -805,19 +842,20 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
 #pragma unroll
             for (int r = 0; r < 16; ++r) o[r] = fmaf(lo[r], 0.0625f, o[r]);
           }
+#pragma unroll
+          for (int r = 0; r < 16; ++r) o[r] = inv[r] > 0.f ? o[r] * inv[r] : 0.f;
         } else {
 #pragma unroll
           for (int r = 0; r < 16; ++r) o[r] = 0.f;
         }
+        if (part >= 0) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          if (r < rows) {
-            const float inv = sm_inv[r0 + r], v = inv > 0.f ? o[r] * inv : 0.f;
-            if (part >= 0)
-              a.o_part[((long long)part * NT + r0 + r) * R + k * 128 + i] = v;
-            else
-              a.out[((long long)b * a.M + R0 + r) * R + k * 128 + i] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
-          }
+          for (int r = 0; r < 16; ++r)
+            if (r < rows) po[r * R] = o[r];
+        } else {
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (r < rows) oo[r * R] = __bfloat16_as_ushort(__float2bfloat16_rn(o[r]));
         }
       }
       tmem_fence_before();
@@ -828,7 +866,6 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
     if (!ok) *abort_flag = 1;
   }
 
-  pdl_launch_dependents();
   tmem_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -839,47 +876,119 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
 }
 
 // Joins the partial results of the sequences that lie in several teams' ranges:
-// lse = ln sum_k exp(lse_k), out = sum_k exp(lse_k - lse) o_k. Block (team, y)
-// takes the cut sequence that starts in the team's range, rows y, y + gridDim.y,
-// ...; its threads are 4 groups of parts x R / 4 columns of four elements.
+// lse = ln sum_k exp(lse_k), out = sum_k exp(lse_k - lse) o_k. The blocks share
+// the rows of all cut sequences: of a sequence of few parts (most cuts leave
+// two) a warp takes a row, with all its loads in flight at once; of one of many
+// parts a block takes a row, four groups of threads with every fourth part each.
+constexpr int kMergeFew = 4, kMergeTeams = 512;
+
 template <int R>
 __global__ void __launch_bounds__(R) latent_merge_kernel(const LatentArgs a, int nt) {
   constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
-  constexpr int CT = R / 4;
+  constexpr unsigned FULL = 0xFFFFFFFFu;
+  constexpr int CT = R / 4, WARPS = R / 32;
   __shared__ float4 part_o[3][CT];
+  __shared__ int2 cuts[kMergeTeams];        // (team, parts) of the cut sequences
+  __shared__ int ends[kMergeTeams], count;  // work items up to and with each
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int few_items = (a.M + WARPS - 1) / WARPS;
   pdl_wait_primary();
-  const int team = blockIdx.x, tid = threadIdx.x, grp = tid / CT, col = tid % CT;
-  const int2 cut = a.cut[team];
-  if (cut.x < 0) return;
-  const int parts = cut.y - team + 1;
-  for (int row = blockIdx.y; row < a.M; row += gridDim.y) {
+  if (warp == 0) {
+    int n = 0, end = 0;
+    for (int t0 = 0; t0 < a.teams; t0 += 32) {
+      const int t = t0 + lane;
+      const int2 c = t < a.teams ? a.cut[t] : make_int2(-1, 0);
+      const int parts = c.x >= 0 ? c.y - t + 1 : 0;
+      int inc = parts == 0 ? 0 : parts <= kMergeFew ? few_items : a.M;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(FULL, inc, o);
+        if (lane >= o) inc += y;
+      }
+      const unsigned live = __ballot_sync(FULL, parts > 0);
+      if (parts > 0) {
+        const int k = n + __popc(live & ((1u << lane) - 1));
+        cuts[k] = make_int2(t, parts);
+        ends[k] = end + inc;
+      }
+      n += __popc(live);
+      end += __shfl_sync(FULL, inc, 31);
+    }
+    if (lane == 0) count = n;
+  }
+  __syncthreads();
+  const int n = count;
+  if (n == 0) return;
+  int c = 0;
+  for (int w = blockIdx.x; w < ends[n - 1]; w += gridDim.x) {
+    while (w >= ends[c]) ++c;
+    const int team = cuts[c].x, parts = cuts[c].y, b = a.cut[team].x;
+    const int in = w - (c > 0 ? ends[c - 1] : 0);
+    const bool few = parts <= kMergeFew;
+    const int row = few ? in * WARPS + warp : in;
+    if (few && row >= a.M) continue;
     const int rt = row / nt, rr = row - rt * nt;
     // slot of part k: the piece goes on behind the team's range but in the last
     auto slot = [&](int k) {
       return ((long long)((team + k) * a.row_tiles + rt) * 2 + (k + 1 < parts ? 1 : 0)) * nt + rr;
     };
-    float m = -INFINITY;
-    for (int k = tid & 31; k < parts; k += 32) m = fmaxf(m, a.lse_part[slot(k)]);
+    float m = -INFINITY, sum = 0.f;
+    const long long o = (long long)b * a.M + row;
+    if (few) {
+      constexpr int V = R / 128;
+      float l[kMergeFew];
+      float4 v[kMergeFew][V];
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    float sum = 0.f;
+      for (int k = 0; k < kMergeFew; ++k) {
+        const long long s = slot(min(k, parts - 1));
+        l[k] = k < parts ? a.lse_part[s] : -INFINITY;
+#pragma unroll
+        for (int x = 0; x < V; ++x)
+          v[k][x] = k < parts ? *reinterpret_cast<const float4*>(a.o_part + s * R + (lane + 32 * x) * 4)
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+        m = fmaxf(m, l[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < kMergeFew; ++k) sum += l[k] == -INFINITY ? 0.f : exp2f((l[k] - m) * kLog2e);
+      const float lse = m == -INFINITY ? -INFINITY : m + log2f(sum) * kLn2;
+#pragma unroll
+      for (int k = 0; k < kMergeFew; ++k) l[k] = l[k] == -INFINITY ? 0.f : exp2f((l[k] - m) * kLog2e) / sum;
+#pragma unroll
+      for (int x = 0; x < V; ++x) {
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kMergeFew; ++k) {
+          acc.x = fmaf(l[k], v[k][x].x, acc.x);
+          acc.y = fmaf(l[k], v[k][x].y, acc.y);
+          acc.z = fmaf(l[k], v[k][x].z, acc.z);
+          acc.w = fmaf(l[k], v[k][x].w, acc.w);
+        }
+        *reinterpret_cast<uint2*>(a.out + o * R + (lane + 32 * x) * 4) =
+            make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+      }
+      if (lane == 0 && a.lse) a.lse[o] = lse;
+      continue;
+    }
+    const int grp = tid / CT, col = tid % CT;
+    for (int k = lane; k < parts; k += 32) m = fmaxf(m, a.lse_part[slot(k)]);
+#pragma unroll
+    for (int x = 16; x >= 1; x >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, x));
     if (m != -INFINITY)
-      for (int k = tid & 31; k < parts; k += 32) sum += exp2f((a.lse_part[slot(k)] - m) * kLog2e);
+      for (int k = lane; k < parts; k += 32) sum += exp2f((a.lse_part[slot(k)] - m) * kLog2e);
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor_sync(FULL, sum, x);
     const float lse = m == -INFINITY ? -INFINITY : m + log2f(sum) * kLn2;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (m != -INFINITY) {
 #pragma unroll 4
       for (int k = grp; k < parts; k += 4) {
         const long long s = slot(k);
-        const float l = a.lse_part[s];
-        const float w = l == -INFINITY ? 0.f : exp2f((l - lse) * kLog2e);
+        const float wgt = exp2f((a.lse_part[s] - m) * kLog2e) / sum;  // 0 for a part without keys
         const float4 v = *reinterpret_cast<const float4*>(a.o_part + s * R + col * 4);
-        acc.x = fmaf(w, v.x, acc.x);
-        acc.y = fmaf(w, v.y, acc.y);
-        acc.z = fmaf(w, v.z, acc.z);
-        acc.w = fmaf(w, v.w, acc.w);
+        acc.x = fmaf(wgt, v.x, acc.x);
+        acc.y = fmaf(wgt, v.y, acc.y);
+        acc.z = fmaf(wgt, v.z, acc.z);
+        acc.w = fmaf(wgt, v.w, acc.w);
       }
     }
     if (grp > 0) part_o[grp - 1][col] = acc;
@@ -893,7 +1002,6 @@ __global__ void __launch_bounds__(R) latent_merge_kernel(const LatentArgs a, int
         acc.z += v.z;
         acc.w += v.w;
       }
-      const long long o = (long long)cut.x * a.M + row;
       *reinterpret_cast<uint2*>(a.out + o * R + col * 4) =
           make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
       if (col == 0 && a.lse) a.lse[o] = lse;
