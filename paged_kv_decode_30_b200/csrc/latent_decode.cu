@@ -57,7 +57,7 @@ Plan make_plan(const pda_latent_params& p, int sms) {
   // One CTA per SM; a team walks a range of tokens with a CTA per row tile.
   // Never more teams than tiles.
   const long long tiles = (long long)p.batch * (((long long)p.max_pages_per_seq * p.page_size + 127) / 128);
-  const long long teams = std::min(sms, 512) / pl.row_tiles;  // 512: what the merge can list
+  const long long teams = std::min(sms, 256) / pl.row_tiles;  // 256: what the merge can list
   pl.teams = (int)(teams < 1 ? 1 : teams < tiles ? teams : tiles);
   const size_t slots = (size_t)pl.teams * pl.row_tiles * 2 * pl.nt;
   pl.lse_off = slots * p.latent_dim * sizeof(float);

@@ -71,8 +71,9 @@ __device__ __forceinline__ void latent_visible(const LatentArgs& a, int L, int i
   lo = (int)(l < 0 ? 0 : (l > L ? L : l));
 }
 
-__device__ __forceinline__ int latent_len(const LatentArgs& a, int b) {
-  return min(max(__ldg(a.kv_lens + b), 0), a.max_pages << a.log2_page);
+// A length from kv_lens, held to what the page table covers.
+__device__ __forceinline__ int latent_len(const LatentArgs& a, int kv_len) {
+  return min(max(kv_len, 0), a.max_pages << a.log2_page);
 }
 
 // First tile and number of tiles that any query row of the sequence sees.
@@ -86,9 +87,9 @@ __device__ __forceinline__ void latent_tiles(const LatentArgs& a, int L, int& fi
 
 // A sequence's share of the line: its tiles, and one unit if it has none, so
 // that some CTA writes its rows.
-__device__ __forceinline__ int latent_weight(const LatentArgs& a, int b) {
+__device__ __forceinline__ int latent_weight(const LatentArgs& a, int kv_len) {
   int first, n;
-  latent_tiles(a, latent_len(a, b), first, n);
+  latent_tiles(a, latent_len(a, kv_len), first, n);
   return max(n, 1);
 }
 
@@ -169,6 +170,23 @@ __device__ __forceinline__ uint32_t sw128(int n, int c) {
   return (n >> 3) * 1024 + (n & 7) * 128 + ((c ^ (n & 7)) << 4);
 }
 
+// mbar_wait that also gives up (without an error of its own) once another role
+// has: the flag is read on the slow path only.
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long start = clock64();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 63u) == 0) {
+      if (*abort_flag) return false;
+      if (clock64() - start > kWaitTimeoutCycles) {
+        record_error_at(err, kErrTimeout);
+        return false;
+      }
+    }
+  }
+}
+
 // One lane of a converged warp (the same one every time).
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -221,30 +239,25 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
   int* sums = reinterpret_cast<int*>(smem + C::OFF_MISC + 16);  // [WARPS]
   LatentItem* items = reinterpret_cast<LatentItem*>(smem + C::OFF_ITEM);
 
-  if (tid == 0) {
-    for (int s = 0; s < C::SLOTS; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
-    }
-    for (int s = 0; s < C::R_SLOTS; ++s) {
-      mbar_init(&rfull[s], 1);
-      mbar_init(&rempty[s], 1);
-    }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&s_full[s], 1);
-      mbar_init(&p_ready[s], C::SOFT_THREADS);
-      mbar_init(&o_full[s], 1);
-    }
-    mbar_init(q_full, FP8 ? C::SOFT_THREADS : 1);
-    mbar_init(q_free, 1);
-    mbar_init(o_free, C::SOFT_THREADS);
-    for (int s = 0; s < C::ITEMS; ++s) {
-      mbar_init(&item_full[s], 32);
-      mbar_init(&item_free[s], C::GROUPS + 3);  // softmax groups, producer, both MMA issuers
-    }
-    *abort_flag = 0;
+  // This thread's sequences' share of the line (the loads go out first).
+  const int chunk = (a.B + C::WARPS - 1) / C::WARPS;
+  int w_sum = 0;  // (the host refuses calls of 2^31 tiles or more)
+  for (int b = warp * chunk + lane; b < min(a.B, (warp + 1) * chunk); b += 32) {
+    const int L = __ldg(a.kv_lens + b);
+    w_sum += latent_weight(a, L);
+    if (blockIdx.x == 0 && (L < 0 || L > (a.max_pages << a.log2_page))) record_error_at(a.err, kErrBadPage);
+  }
+  if (tid < C::BARS) {
+    uint64_t* bar = full + tid;
+    const uint32_t count = bar >= p_ready && bar < o_full                 ? C::SOFT_THREADS
+                           : bar == o_free || (FP8 && bar == q_full)      ? C::SOFT_THREADS
+                           : bar >= item_full && bar < item_free          ? 32
+                           : bar >= item_free ? C::GROUPS + 3  // softmax groups, producer, both MMA issuers
+                                              : 1;
+    mbar_init(bar, count);
     fence_mbar_init();
   }
+  if (tid == 0) *abort_flag = 0;
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_addr(tmem_slot)),
@@ -252,18 +265,8 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  // Each warp adds up one chunk of the sequences' weights.
-  const int chunk = (a.B + C::WARPS - 1) / C::WARPS;
-  {
-    int w = 0;  // (the host refuses calls of 2^31 tiles or more)
-    for (int b = warp * chunk + lane; b < min(a.B, (warp + 1) * chunk); b += 32) {
-      w += latent_weight(a, b);
-      const int L = __ldg(a.kv_lens + b);
-      if (blockIdx.x == 0 && (L < 0 || L > (a.max_pages << a.log2_page))) record_error_at(a.err, kErrBadPage);
-    }
-    w = __reduce_add_sync(FULL, w);
-    if (lane == 0) sums[warp] = w;
-  }
+  w_sum = __reduce_add_sync(FULL, w_sum);
+  if (lane == 0) sums[warp] = w_sum;
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
@@ -275,69 +278,77 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
     // The line's length and this team's range [s, e) of it (a line shorter than
     // the number of teams leaves the last ones idle, so that no range is empty);
     // then every sequence that overlaps the range becomes an item.
-    int total = lane < C::WARPS ? sums[lane] : 0;
-    total = __reduce_add_sync(FULL, total);
+    int upto = lane < C::WARPS ? sums[lane] : 0;  // up to and with warp `lane`'s chunk
+    const int own_sum = upto;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(FULL, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const int total = __shfl_sync(FULL, upto, 31);
     // the first `more` teams take share + 1 units, the rest share
     const int teams = min(a.teams, total), share = total / teams, more = total - share * teams;
     const int s = team < teams ? share * team + min(team, more) : total;
     const int e = team < teams ? s + share + (team < more ? 1 : 0) : 0;
-    int at = 0;  // where the sequences looked at next begin
+    const int i0 = rt * NT / a.H, i1 = (min(a.M, rt * NT + NT) - 1) / a.H;  // query rows of the row tile
     int j = 0;
     bool ok = true;
-    int2 cut = make_int2(-1, 0);
-    auto publish = [&](int b, int begin, int w) {  // uniform over the warp
-      ok = ok && !*abort_flag;
-      if (ok && j >= C::ITEMS) ok = mbar_wait(&item_free[j % C::ITEMS], ((j / C::ITEMS) - 1) & 1, a.err);
-      if (!__all_sync(FULL, ok)) {
-        ok = false;
-        return;
-      }
+    int cut_b = -1, cut_last = 0;  // the cut sequence that starts here and the unit of its last tile
+    auto publish = [&](int b, int kv_len, int begin, int w) {  // uniform over the warp
+      if (j >= C::ITEMS)
+        ok = __all_sync(FULL, wait_or_abort(&item_free[j % C::ITEMS], ((j / C::ITEMS) - 1) & 1, abort_flag, a.err));
+      if (!ok) return;
       LatentItem& d = items[j % C::ITEMS];
-      if (lane == 0) {
-        d.b = b;
-        if (b >= 0) {
-          const int L = latent_len(a, b);
-          int first, n;
-          latent_tiles(a, L, first, n);
-          const int t0 = max(s, begin) - begin, t1 = min(e, begin + w) - begin;
+      if (b >= 0) {
+        const int L = latent_len(a, kv_len), t0 = max(s, begin) - begin, t1 = min(e, begin + w) - begin;
+        const bool whole = t0 == 0 && t1 == w;
+        int first, n;
+        latent_tiles(a, L, first, n);
+        int lo_u, hi_u, lo_x, hi_x;
+        latent_visible(a, L, i0, lo_u, hi_x);
+        latent_visible(a, L, i1, lo_x, hi_u);
+        if (lane == 0) {
+          d.b = b;
           d.L = L;
           d.first = first + t0;
           d.n = n == 0 ? 0 : t1 - t0;
-          const bool whole = t0 == 0 && t1 == w;
           // a team's range holds at most one cut piece that ends in it (its
           // first) and one that goes on behind it (its last)
           d.part = whole ? -1 : (team * a.row_tiles + rt) * 2 + (begin + w > e ? 1 : 0);
-          if (t0 == 0 && !whole) {  // the team of the sequence's last tile
-            const int last = begin + w - 1, wide = (share + 1) * more;
-            cut = make_int2(b, last < wide ? last / (share + 1) : more + (last - wide) / share);
-          }
-          const int R0 = rt * NT, R1 = min(a.M, R0 + NT) - 1;
-          latent_visible(a, L, R0 / a.H, d.lo_u, d.hi_x);
-          latent_visible(a, L, R1 / a.H, d.lo_x, d.hi_u);
+          d.lo_u = lo_u;
+          d.hi_u = hi_u;
+          d.lo_x = lo_x;
+          d.hi_x = hi_x;
         }
+        if (t0 == 0 && !whole) {
+          cut_b = b;
+          cut_last = begin + w - 1;
+        }
+      } else if (lane == 0) {
+        d.b = -1;
       }
       __syncwarp();
       mbar_arrive(&item_full[j % C::ITEMS]);
       if (!FP8 && b >= 0) {  // Q rows by TMA, once the item before has been multiplied
-        if (j >= 1) ok = mbar_wait(q_free, (j - 1) & 1, a.err);
-        ok = __all_sync(FULL, ok);
+        if (j >= 1) ok = __all_sync(FULL, wait_or_abort(q_free, (j - 1) & 1, abort_flag, a.err));
         if (ok && lane == 0) {
           mbar_arrive_expect_tx(q_full, C::Q_BYTES);
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c <= R / 64; ++c)
             tma_load_2d(sbase + C::OFF_Q + c * (NT * 128), &map_q, c * 64, b * a.M + rt * NT, q_full);
         }
+        __syncwarp();
       }
       ++j;
     };
-    for (int w = 0; w < C::WARPS && ok && at < e; ++w) {
-      if (at + sums[w] <= s) {
-        at += sums[w];
-        continue;
-      }
+    // the chunk that holds unit s, then on to the range's end
+    int w = __ffs(__ballot_sync(FULL, s < e && upto > s)) - 1;
+    int at = w >= 0 ? __shfl_sync(FULL, upto - own_sum, w) : 0;  // where the sequences looked at next begin
+    for (; w >= 0 && w < C::WARPS && ok && at < e; ++w) {
       const int b1 = min(a.B, (w + 1) * chunk);
       for (int b0 = w * chunk; b0 < b1 && ok && at < e; b0 += 32) {
-        const int wt = b0 + lane < b1 ? latent_weight(a, b0 + lane) : 0;
+        const int len = b0 + lane < b1 ? __ldg(a.kv_lens + b0 + lane) : 0;
+        const int wt = b0 + lane < b1 ? latent_weight(a, len) : 0;
         int inc = wt;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -349,14 +360,17 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
         while (hit && ok) {
           const int src = __ffs(hit) - 1;
           hit &= hit - 1;
-          publish(b0 + src, __shfl_sync(FULL, begin, src), __shfl_sync(FULL, wt, src));
+          publish(b0 + src, __shfl_sync(FULL, len, src), __shfl_sync(FULL, begin, src), __shfl_sync(FULL, wt, src));
         }
         at += __shfl_sync(FULL, inc, 31);
       }
     }
-    if (ok) publish(-1, 0, 0);
+    if (ok) publish(-1, 0, 0, 0);
     if (!ok) *abort_flag = 1;
-    if (rt == 0 && lane == 0) a.cut[team] = cut;
+    if (rt == 0 && lane == 0) {  // the team of the cut sequence's last tile
+      const int wide = (share + 1) * more;
+      a.cut[team] = make_int2(cut_b, cut_last < wide ? cut_last / (share + 1) : more + (cut_last - wide) / share);
+    }
     __syncwarp();
   } else if (warp == 0) {
     // ======================= TMA producer (whole warp) =========================
@@ -370,7 +384,7 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
     int g = 0, blk = 0;
     bool ok = true;
     for (int j = 0; ok; ++j) {
-      ok = __all_sync(FULL, !*abort_flag && mbar_wait(&item_full[j % C::ITEMS], (j / C::ITEMS) & 1, a.err));
+      ok = __all_sync(FULL, wait_or_abort(&item_full[j % C::ITEMS], (j / C::ITEMS) & 1, abort_flag, a.err));
       if (!ok) break;
       const LatentItem d = items[j % C::ITEMS];
       __syncwarp();
@@ -400,10 +414,10 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
 #pragma unroll 1
         for (int k = 0; k < C::NB; ++k, ++blk) {
           const int sl = blk % C::SLOTS;
-          ok = !*abort_flag;
-          if (ok && blk >= C::SLOTS) ok = mbar_wait(&empty[sl], ((blk / C::SLOTS) - 1) & 1, a.err);
-          ok = __all_sync(FULL, ok);
-          if (!ok) break;
+          if (blk >= C::SLOTS) {
+            ok = __all_sync(FULL, wait_or_abort(&empty[sl], ((blk / C::SLOTS) - 1) & 1, abort_flag, a.err));
+            if (!ok) break;
+          }
           if (lane == 0) mbar_arrive_expect_tx(&full[sl], FP8 ? bytes : 2 * bytes);
           __syncwarp();
           if (lane < nseg) {
@@ -414,10 +428,10 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
         }
         if (!ok) break;
         const int rs = g % C::R_SLOTS;
-        ok = !*abort_flag;
-        if (ok && g >= C::R_SLOTS) ok = mbar_wait(&rempty[rs], ((g / C::R_SLOTS) - 1) & 1, a.err);
-        ok = __all_sync(FULL, ok);
-        if (!ok) break;
+        if (g >= C::R_SLOTS) {
+          ok = __all_sync(FULL, wait_or_abort(&rempty[rs], ((g / C::R_SLOTS) - 1) & 1, abort_flag, a.err));
+          if (!ok) break;
+        }
         if (lane == 0) mbar_arrive_expect_tx(&rfull[rs], bytes);
         __syncwarp();
         if (lane < nseg) tma_load_2d(sbase + C::OFF_ROPE + rs * C::ROPE_SLOT + off, &map_r, 0, row, &rfull[rs]);
@@ -446,23 +460,23 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
     int g = 0, blk = 0, issued = 0;
     auto agreed = [&](bool v) { return __all_sync(FULL, v); };
     for (int j = 0; ok; ++j) {
-      ok = agreed(!*abort_flag && mbar_wait(&item_full[j % C::ITEMS], (j / C::ITEMS) & 1, a.err));
+      ok = agreed(wait_or_abort(&item_full[j % C::ITEMS], (j / C::ITEMS) & 1, abort_flag, a.err));
       if (!ok) break;
       const int n = items[j % C::ITEMS].n, b = items[j % C::ITEMS].b;
       __syncwarp();
       if (lane == 0) mbar_arrive(&item_free[j % C::ITEMS]);
       if (b < 0) break;
       if (warp == 1) {
-        ok = agreed(mbar_wait(q_full, j & 1, a.err));
+        ok = agreed(wait_or_abort(q_full, j & 1, abort_flag, a.err));
         for (int t = 0; ok && t < n; ++t, ++g) {
           const int bb = g & 1;
-          if (g >= 2) ok = agreed(!*abort_flag && mbar_wait(&p_ready[bb], ((g - 2) >> 1) & 1, a.err));
+          if (g >= 2) ok = agreed(wait_or_abort(&p_ready[bb], ((g - 2) >> 1) & 1, abort_flag, a.err));
           const uint32_t dt = tmem + C::COL_S + bb * C::SN;
           const uint64_t q0 = umma_desc(sbase + C::OFF_Q, 16, 1024, kSw128);
 #pragma unroll 1
           for (int k = 0; ok && k < C::NB; ++k, ++blk) {
             const int sl = blk % C::SLOTS;
-            ok = agreed(!*abort_flag && mbar_wait(&full[sl], (blk / C::SLOTS) & 1, a.err));
+            ok = agreed(wait_or_abort(&full[sl], (blk / C::SLOTS) & 1, abort_flag, a.err));
             if (!ok) break;
             tmem_fence_after();
             const uint64_t ca = umma_desc(sbase + C::OFF_BLK + sl * C::BLK, 16, 1024, kSw128);
@@ -483,7 +497,7 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
             __syncwarp();
           }
           const int rs = g % C::R_SLOTS;
-          ok = agreed(ok && !*abort_flag && mbar_wait(&rfull[rs], (g / C::R_SLOTS) & 1, a.err));
+          ok = agreed(ok && wait_or_abort(&rfull[rs], (g / C::R_SLOTS) & 1, abort_flag, a.err));
           if (!ok) break;
           tmem_fence_after();
           if (leader) {
@@ -501,10 +515,10 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
         }
         if (ok && leader) umma_commit(q_free);
       } else {
-        if (j >= 1) ok = agreed(mbar_wait(o_free, (j - 1) & 1, a.err));
+        if (j >= 1) ok = agreed(wait_or_abort(o_free, (j - 1) & 1, abort_flag, a.err));
         for (int t = 0; ok && t < n; ++t, ++g) {
           const int bb = g & 1;
-          ok = agreed(!*abort_flag && mbar_wait(&p_ready[bb], (g >> 1) & 1, a.err));
+          ok = agreed(wait_or_abort(&p_ready[bb], (g >> 1) & 1, abort_flag, a.err));
           if (!ok) break;
           tmem_fence_after();
           constexpr uint32_t SBO = 8 * C::P_ROW;
@@ -566,7 +580,7 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
     int g = 0;
     bool ok = true;
     for (int j = 0; ok; ++j) {
-      const bool got = !*abort_flag && mbar_wait(&item_full[j % C::ITEMS], (j / C::ITEMS) & 1, a.err);
+      const bool got = wait_or_abort(&item_full[j % C::ITEMS], (j / C::ITEMS) & 1, abort_flag, a.err);
       if (!named_bar_and(gbar, GT, got)) {
         ok = false;
         break;
@@ -655,7 +669,7 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
         const int bb = g & 1;
         const float e_tok = FP8 ? (float)(min(max(sc_next, 97), 157) - 127) : 0.f;
         sc_next = scale_of(t + 1);
-        bool good = __all_sync(FULL, !*abort_flag && mbar_wait(&s_full[bb], (g >> 1) & 1, a.err));
+        bool good = __all_sync(FULL, wait_or_abort(&s_full[bb], (g >> 1) & 1, abort_flag, a.err));
         float x[16];
         if (good) {
           tmem_fence_after();
@@ -831,7 +845,7 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
       for (int r = 0; r < 16; ++r) inv[r] = sm_inv[r0 + r];
       float* po = a.o_part + ((long long)part * NT + r0) * R + i;
       uint16_t* oo = a.out + ((long long)b * a.M + R0) * R + i;
-#pragma unroll 1
+#pragma unroll (NT == 64 ? 1 : 2)
       for (int k = 0; k < C::NB; ++k, po += 128, oo += 128) {
         float o[16];
         if (n > 0) {
@@ -880,10 +894,10 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
 // the rows of all cut sequences: of a sequence of few parts (most cuts leave
 // two) a warp takes a row, with all its loads in flight at once; of one of many
 // parts a block takes a row, four groups of threads with every fourth part each.
-constexpr int kMergeFew = 4, kMergeTeams = 512;
+constexpr int kMergeFew = 4, kMergeTeams = 256;
 
 template <int R>
-__global__ void __launch_bounds__(R) latent_merge_kernel(const LatentArgs a, int nt) {
+__global__ void __launch_bounds__(R, 1024 / R) latent_merge_kernel(const LatentArgs a, int nt) {
   constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
   constexpr unsigned FULL = 0xFFFFFFFFu;
   constexpr int CT = R / 4, WARPS = R / 32;
@@ -937,15 +951,12 @@ __global__ void __launch_bounds__(R) latent_merge_kernel(const LatentArgs a, int
     if (few) {
       constexpr int V = R / 128;
       float l[kMergeFew];
-      float4 v[kMergeFew][V];
+      const float4* src[kMergeFew];
 #pragma unroll
       for (int k = 0; k < kMergeFew; ++k) {
         const long long s = slot(min(k, parts - 1));
         l[k] = k < parts ? a.lse_part[s] : -INFINITY;
-#pragma unroll
-        for (int x = 0; x < V; ++x)
-          v[k][x] = k < parts ? *reinterpret_cast<const float4*>(a.o_part + s * R + (lane + 32 * x) * 4)
-                              : make_float4(0.f, 0.f, 0.f, 0.f);
+        src[k] = reinterpret_cast<const float4*>(a.o_part + s * R) + lane;
         m = fmaxf(m, l[k]);
       }
 #pragma unroll
@@ -953,15 +964,17 @@ __global__ void __launch_bounds__(R) latent_merge_kernel(const LatentArgs a, int
       const float lse = m == -INFINITY ? -INFINITY : m + log2f(sum) * kLn2;
 #pragma unroll
       for (int k = 0; k < kMergeFew; ++k) l[k] = l[k] == -INFINITY ? 0.f : exp2f((l[k] - m) * kLog2e) / sum;
-#pragma unroll
+#pragma unroll 2
       for (int x = 0; x < V; ++x) {
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f), v[kMergeFew];
+#pragma unroll
+        for (int k = 0; k < kMergeFew; ++k) v[k] = k < parts ? src[k][32 * x] : acc;
 #pragma unroll
         for (int k = 0; k < kMergeFew; ++k) {
-          acc.x = fmaf(l[k], v[k][x].x, acc.x);
-          acc.y = fmaf(l[k], v[k][x].y, acc.y);
-          acc.z = fmaf(l[k], v[k][x].z, acc.z);
-          acc.w = fmaf(l[k], v[k][x].w, acc.w);
+          acc.x = fmaf(l[k], v[k].x, acc.x);
+          acc.y = fmaf(l[k], v[k].y, acc.y);
+          acc.z = fmaf(l[k], v[k].z, acc.z);
+          acc.w = fmaf(l[k], v[k].w, acc.w);
         }
         *reinterpret_cast<uint2*>(a.out + o * R + (lane + 32 * x) * 4) =
             make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));

@@ -58,7 +58,7 @@ cudaError_t launch_latent(const LatentCall& c, cudaStream_t stream) {
   e = cudaGetLastError();
   if (e != cudaSuccess || a.teams == 1) return e;  // one team cuts no sequence
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(4 * a.teams * a.row_tiles < 592 ? 4 * a.teams * a.row_tiles : 592));
+  cfg.gridDim = dim3((unsigned)(a.teams * a.row_tiles * (1024 / R)));
   cfg.blockDim = dim3(R);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
