@@ -1,0 +1,462 @@
+// Attention over an expanded latent cache on the 5th-generation tensor cores:
+// ragged query rows against keys [k_nope(head) | k_rope(shared)] and values of
+// each head, with causal and window masks.
+//
+// A CTA takes 256 query rows of one sequence and head as two tiles A and B of
+// 128 (the M dimension) and walks the keys 128 at a time:
+//   S = Q K^T   [128, 128 keys]   K: 128 + 64 elements, both from shared memory
+//   O += P V    [128, 128 dims]   K: 128 keys, P from TMEM, V from shared memory
+// S (2 x 128 columns) and O (2 x 128) fill TMEM; the weights P, bf16, take the
+// first 64 columns of their S. The two tiles run half a step apart: while the
+// softmax warps of one tile work, the tensor core has the other tile's products,
+//   P_A V(t), Q_A K(t + 1), P_B V(t), Q_B K(t + 1), ...
+// The products of a CTA execute in the order in which they are issued, so Q_A
+// K(t + 1) overwrites the weights that P_A V(t) has read.
+//
+// Bounds: a step of both tiles is 2 x (12 x 68 + 8 x 64) = 2656 tensor cycles
+// (an M = N = 128 product of 16 takes 64, 68 with both operands from shared
+// memory), and 2 x 128 x 128 exponentials, 2048 cycles of the special function
+// units: the tensor core is the bound, closely followed by the exponentials.
+//
+// Shared memory: Q 96 KB, two stages of K (48 KB each) and one V (32 KB, freed
+// and filled in halves of 64 keys). No room for a second V.
+//
+// Roles (warps): 0 TMA producer, 1 MMA issuer (which also zeroes the V rows
+// that no query row sees: they may hold NaN, which a zero weight does not
+// cancel), 2-3 idle; 4-7 softmax of tile A, 8-11 of tile B, a thread a query
+// row. Every wait is bounded.
+#pragma once
+
+#include "pda_device.cuh"
+#include "split_tma.cuh"  // instruction descriptors
+#include "tcgen05.cuh"
+
+namespace pda {
+
+struct PrefillArgs {
+  const int32_t* q_offsets;
+  const int32_t* kv_offsets;
+  uint16_t* out;  // bf16 [total_q, H, 128]
+  float* lse;     // [total_q, H] or null
+  int* err;
+  int B, H, total_q, total_kv, max_q, tiles, causal_offset, window;
+  float scale_log2;
+};
+
+struct PrefillCfg {
+  static constexpr int D = 128, QT = 128, KT = 128;
+  static constexpr int CHUNK = 128 * 128;            // 128 rows of 64 bf16
+  static constexpr int OFF_Q = 0;                    // 2 tiles x 3 chunks
+  static constexpr int OFF_K = OFF_Q + 6 * CHUNK;    // 2 stages x 3 chunks
+  static constexpr int OFF_V = OFF_K + 6 * CHUNK;    // 2 chunks
+  static constexpr int OFF_BAR = OFF_V + 2 * CHUNK;
+  // q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2]
+  static constexpr int BARS = 16;
+  static constexpr int OFF_MISC = OFF_BAR + BARS * 8;
+  static constexpr int SMEM_ALLOC = OFF_MISC + 16 + 1024;
+  static constexpr int THREADS = 384;
+  static constexpr int COL_S = 0, COL_O = 256;
+  static_assert(SMEM_ALLOC <= 227 * 1024, "shared memory");
+};
+
+// Keys [lo, hi) that query row i of a sequence of nq rows and nk keys sees.
+__device__ __forceinline__ void prefill_visible(const PrefillArgs& a, int nq, int nk, int i, int& lo, int& hi) {
+  long long pos = (long long)nk - 1;
+  if (a.causal_offset >= 0) pos = (long long)a.causal_offset + i;
+  else if (a.causal_offset == -2) pos = (long long)nk - nq + i;
+  const long long h = a.causal_offset != -1 ? pos + 1 : (long long)nk;
+  const long long l = a.window > 0 ? pos - a.window + 1 : 0;
+  hi = (int)(h < 0 ? 0 : (h > nk ? nk : h));
+  lo = (int)(l < 0 ? 0 : (l > nk ? nk : l));
+}
+
+// D += A B with A (bf16, K-major) in TMEM.
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// 32 consecutive TMEM columns of this thread's lane; the caller waits
+// (tmem_wait_ld) before it uses them.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+// Waits for this thread's TMEM loads; the registers pass through so that no use moves above it.
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__global__ void __launch_bounds__(PrefillCfg::THREADS, 1)
+    latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_kv,
+                          const __grid_constant__ CUtensorMap map_r, const PrefillArgs a) {
+  using C = PrefillCfg;
+  constexpr unsigned FULL = 0xFFFFFFFFu;
+  // Heads vary fastest, so that the CTAs of one time read few sequences' keys;
+  // the last tiles come first: with a causal mask they see the most keys.
+  const int h = blockIdx.x % a.H, y = blockIdx.x / a.H, b = y % a.B, tile = a.tiles - 1 - y / a.B;
+  const int qb = __ldg(a.q_offsets + b), nq_all = __ldg(a.q_offsets + b + 1) - qb;
+  const int kb = __ldg(a.kv_offsets + b), nk = __ldg(a.kv_offsets + b + 1) - kb;
+  if (qb < 0 || nq_all < 0 || nq_all > a.total_q - qb || kb < 0 || nk < 0 || nk > a.total_kv - kb) {
+    if (threadIdx.x == 0) record_error_at(a.err, kErrBadPage);
+    return;
+  }
+  const int row0 = tile * 2 * C::QT, rows = min(min(nq_all, a.max_q) - row0, 2 * C::QT);
+  if (rows <= 0) return;
+
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = smem_addr(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // [tile]
+  uint64_t* k_full = q_full + 2;   // [stage]
+  uint64_t* k_empty = k_full + 2;  // [stage]
+  uint64_t* v_full = k_empty + 2;  // [half]
+  uint64_t* v_empty = v_full + 2;  // [half]
+  uint64_t* s_full = v_empty + 2;  // [tile] S in TMEM, and the products before it done
+  uint64_t* p_full = s_full + 2;   // [tile] weights in TMEM
+  uint64_t* o_full = p_full + 2;   // [tile] all products done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+
+  // Key tiles [t0, t1) of either query tile, and keys [lo, hi) that any row sees.
+  int t0[2], t1[2], lo_u = 0, hi_u = 0;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int first = row0 + x * C::QT, last = row0 + min(rows, (x + 1) * C::QT) - 1;
+    t0[x] = t1[x] = 0;
+    if (last >= first) {
+      int lo, hi, z;
+      prefill_visible(a, nq_all, nk, first, lo, z);
+      prefill_visible(a, nq_all, nk, last, z, hi);
+      if (hi > lo) {
+        t0[x] = lo / C::KT;
+        t1[x] = (hi + C::KT - 1) / C::KT;
+        if (hi_u == 0) lo_u = lo;
+        hi_u = max(hi_u, hi);
+      }
+    }
+  }
+  const bool has_a = t1[0] > t0[0], has_b = t1[1] > t0[1];
+  const int tb = has_a && has_b ? min(t0[0], t0[1]) : has_a ? t0[0] : t0[1];
+  const int te = has_a && has_b ? max(t1[0], t1[1]) : has_a ? t1[0] : t1[1];
+  auto active = [&](int x, int t) { return t >= t0[x] && t < t1[x]; };
+  // keys of tile t that no row sees must not meet the product as NaN
+  auto ragged = [&](int t) { return t * C::KT < lo_u || (t + 1) * C::KT > hi_u; };
+
+  if (tid < C::BARS) {
+    uint64_t* bar = q_full + tid;
+    mbar_init(bar, bar >= p_full && bar < o_full ? 128 : 1);
+    fence_mbar_init();
+  }
+  if (tid == 0) *abort_flag = 0;
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(tmem_slot)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // Registers: 384 x 168 at launch; the softmax warps hold a row of 128 scores.
+  // 4 x 32 x 72 + 8 x 32 x 208 = 62464 of 64512.
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 0) {
+      // ======================= TMA producer (one lane) =========================
+      if (lane == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_kv) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_r) : "memory");
+        bool ok = true;
+        auto load_q = [&](int x) {
+          mbar_arrive_expect_tx(&q_full[x], 3 * C::CHUNK);
+          for (int c = 0; c < 3; ++c)
+            tma_load_3d(sbase + C::OFF_Q + (3 * x + c) * C::CHUNK, &map_q, 64 * c, h, qb + row0 + x * C::QT, &q_full[x]);
+        };
+        auto load_k = [&](int t) {
+          const int n = t - tb, st = n & 1;
+          if (n >= 2) ok = ok && wait_or_abort(&k_empty[st], ((n >> 1) - 1) & 1, abort_flag, a.err);
+          if (!ok) return;
+          const uint32_t dst = sbase + C::OFF_K + st * 3 * C::CHUNK;
+          mbar_arrive_expect_tx(&k_full[st], 3 * C::CHUNK);
+          for (int x = 0; x < 4; ++x)  // (64-element column, 64 keys)
+            tma_load_3d(dst + (x >> 1) * C::CHUNK + (x & 1) * (C::CHUNK / 2), &map_kv, (x >> 1) * 64, h,
+                        kb + t * C::KT + (x & 1) * 64, &k_full[st]);
+          tma_load_2d(dst + 2 * C::CHUNK, &map_r, 0, kb + t * C::KT, &k_full[st]);
+        };
+        if (has_a) load_q(0);
+        if (te > tb) load_k(tb);
+        if (has_b) load_q(1);
+        int vloads = 0;
+        for (int t = tb; ok && t < te; ++t) {
+          if (t + 1 < te) load_k(t + 1);
+          for (int half = 0; ok && half < 2; ++half) {
+            const int n = t - tb;
+            if (n >= 1) ok = wait_or_abort(&v_empty[half], (n - 1) & 1, abort_flag, a.err);
+            if (!ok) break;
+            const uint32_t dst = sbase + C::OFF_V + half * (C::CHUNK / 2);
+            mbar_arrive_expect_tx(&v_full[half], C::CHUNK);
+            tma_load_3d(dst, &map_kv, C::D, h, kb + t * C::KT + half * 64, &v_full[half]);
+            tma_load_3d(dst + C::CHUNK, &map_kv, C::D + 64, h, kb + t * C::KT + half * 64, &v_full[half]);
+          }
+          vloads = t - tb + 1;
+        }
+        if (!ok) {  // copies already issued land before the CTA's shared memory goes away
+          *abort_flag = 1;
+          const long long lim = kWaitTimeoutCycles / 16;
+          if (has_a) mbar_wait(&q_full[0], 0, a.err, lim);
+          if (has_b) mbar_wait(&q_full[1], 0, a.err, lim);
+          for (int n = max(0, vloads - 1); n < vloads + 1; ++n) {
+            mbar_wait(&k_full[n & 1], (n >> 1) & 1, a.err, lim);
+            mbar_wait(&v_full[0], n & 1, a.err, lim);
+            mbar_wait(&v_full[1], n & 1, a.err, lim);
+          }
+        }
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ======================= MMA issuer =======================================
+      const bool leader = elect_one();
+      bool ok = true;
+      int issued[2] = {0, 0};  // S products so far
+      auto agreed = [&](bool v) { return __all_sync(FULL, v); };
+      auto scores = [&](int x, int t) {  // S_x = Q_x K(t)^T
+        const int st = (t - tb) & 1;
+        ok = ok && agreed(wait_or_abort(&k_full[st], ((t - tb) >> 1) & 1, abort_flag, a.err));
+        if (ok && t == t0[x]) ok = agreed(wait_or_abort(&q_full[x], 0, abort_flag, a.err));
+        if (!ok) return;
+        tmem_fence_after();
+        if (leader) {
+          constexpr uint32_t idesc = umma_idesc_bf16(128, 128, false, false);
+          const uint64_t qd = umma_desc(sbase + C::OFF_Q + x * 3 * C::CHUNK, 16, 1024, kSw128);
+          const uint64_t kd = umma_desc(sbase + C::OFF_K + st * 3 * C::CHUNK, 16, 1024, kSw128);
+#pragma unroll
+          for (int s = 0; s < 12; ++s) {
+            const int off = ((s >> 2) * C::CHUNK + (s & 3) * 32) >> 4;
+            umma_f16(tmem + C::COL_S + x * 128, qd + off, kd + off, idesc, s > 0);
+          }
+          umma_commit(&s_full[x]);
+        }
+        __syncwarp();
+        ++issued[x];
+      };
+      auto values = [&](int x, int t, bool last_reader) {  // O_x += P_x V(t)
+        ok = ok && agreed(wait_or_abort(&p_full[x], (t - t0[x]) & 1, abort_flag, a.err));
+        const uint64_t vd = umma_desc(sbase + C::OFF_V, C::CHUNK, 1024, kSw128);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          ok = ok && agreed(wait_or_abort(&v_full[half], (t - tb) & 1, abort_flag, a.err));
+          if (!ok) return;
+          tmem_fence_after();
+          if (leader) {
+            constexpr uint32_t idesc = umma_idesc_bf16(128, 128, false, true);
+#pragma unroll
+            for (int s = 4 * half; s < 4 * half + 4; ++s)
+              umma_f16_ts(tmem + C::COL_O + x * 128, tmem + C::COL_S + x * 128 + 8 * s, vd + ((s * 2048) >> 4),
+                          idesc, t > t0[x] || s > 0);
+            if (last_reader) umma_commit(&v_empty[half]);
+          }
+          __syncwarp();
+        }
+        if (t + 1 == t1[x]) {
+          if (leader) umma_commit(&o_full[x]);
+          __syncwarp();
+        }
+      };
+      if (te > tb) {
+        if (active(0, tb)) scores(0, tb);
+        if (active(1, tb)) scores(1, tb);
+        if (ok && leader) umma_commit(&k_empty[0]);
+        __syncwarp();
+      }
+      for (int t = tb; ok && t < te; ++t) {
+        if (ragged(t)) {  // V rows that no query row sees become zeros
+          ok = agreed(wait_or_abort(&v_full[0], (t - tb) & 1, abort_flag, a.err) &&
+                      wait_or_abort(&v_full[1], (t - tb) & 1, abort_flag, a.err));
+          if (!ok) break;
+          for (int r = lane; r < C::KT; r += 32) {
+            const int key = t * C::KT + r;
+            if (key >= lo_u && key < hi_u) continue;
+            uint8_t* row = smem + C::OFF_V + r * 128;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const int cc = (c + r) & 7;
+              *reinterpret_cast<uint4*>(row + cc * 16) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(row + C::CHUNK + cc * 16) = make_uint4(0, 0, 0, 0);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        const bool next = t + 1 < te;
+        if (ok && active(0, t)) values(0, t, !active(1, t));
+        if (ok && next && active(0, t + 1)) scores(0, t + 1);
+        if (ok && active(1, t)) values(1, t, true);
+        if (ok && next && active(1, t + 1)) scores(1, t + 1);
+        if (ok && next && leader) umma_commit(&k_empty[(t + 1 - tb) & 1]);
+        __syncwarp();
+      }
+      if (!ok) *abort_flag = 1;
+      if (*abort_flag) {  // MMAs already issued finish before TMEM is freed
+        if (leader) umma_commit(&v_empty[0]);
+        for (int x = 0; x < 2; ++x)
+          if (issued[x] > 0) mbar_wait(&s_full[x], (issued[x] - 1) & 1, a.err, kWaitTimeoutCycles / 16);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ======================= softmax: a thread a query row ======================
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    constexpr float kLn2 = 0.69314718055994531f, kUnset = -1e30f;
+    const int x = (warp - 4) >> 2, q4 = warp & 3, r = 32 * q4 + lane;
+    const int i = row0 + x * C::QT + r;
+    const bool live = x * C::QT + r < rows;
+    const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
+    const uint32_t s_tm = tmem + lane_off + C::COL_S + x * 128, o_tm = tmem + lane_off + C::COL_O + x * 128;
+    int lo = 0, hi = 0;
+    if (live) prefill_visible(a, nq_all, nk, i, lo, hi);
+    float m = kUnset, l = 0.f;
+    bool ok = true;
+    for (int t = t0[x]; t < t1[x]; ++t) {
+      ok = __all_sync(FULL, wait_or_abort(&s_full[x], (t - t0[x]) & 1, abort_flag, a.err));
+      if (!ok) break;
+      tmem_fence_after();
+      uint32_t s[128];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32_async(s_tm + 32 * c, s + 32 * c);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_wait_ld32(s + 32 * c);
+      const int j0 = t * C::KT;
+      if (__any_sync(FULL, lo > j0 || hi < j0 + C::KT)) {
+#pragma unroll
+        for (int k = 0; k < 128; ++k)
+          if (j0 + k < lo || j0 + k >= hi) s[k] = 0xFF800000u;  // -inf
+      }
+      float mx[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mx[k] = __uint_as_float(s[k]);
+#pragma unroll
+      for (int k = 4; k < 128; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(s[k]));
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+      // The running maximum moves only when a weight would pass 2^8; the warp
+      // then moves what its rows have added up so far.
+      if (__any_sync(FULL, top - m > 8.f)) {
+        const float m_new = fmaxf(m, top), al = fast_exp2(m - m_new);
+        m = m_new;
+        l *= al;
+        if (t > t0[x]) {  // O is idle: S of this tile was ready after all products before it
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tmem_ld32_async(o_tm + 32 * c, o);
+            tmem_wait_ld32(o);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
+            tmem_st32(o_tm + 32 * c, o);
+          }
+        }
+      }
+      const f32x2 sc2 = f2_pack(a.scale_log2, a.scale_log2), nm2 = f2_pack(-m, -m);
+      f32x2 sum2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+      uint32_t p[64];
+#pragma unroll
+      for (int k = 0; k < 128; k += 2) {
+        float u, v;
+        f2_unpack(f2_fma(f2_pack(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), sc2, nm2), u, v);
+        u = fast_exp2(u);
+        v = fast_exp2(v);
+        sum2[(k >> 1) & 1] = f2_add(sum2[(k >> 1) & 1], f2_pack(u, v));
+        p[k >> 1] = pack_bf16x2(u, v);
+        if ((k & 63) == 62) tmem_st32(s_tm + (k >> 6) * 32, p + (k >> 6) * 32);
+      }
+      float u, v;
+      f2_unpack(f2_add(sum2[0], sum2[1]), u, v);
+      l += u + v;
+      tmem_wait_st();
+      tmem_fence_before();
+      mbar_arrive(&p_full[x]);
+    }
+    if (!ok) *abort_flag = 1;
+    // ---- normalise and store --------------------------------------------------
+    const bool any = t1[x] > t0[x];
+    if (ok && any) ok = wait_or_abort(&o_full[x], 0, abort_flag, a.err);
+    ok = __all_sync(FULL, ok);
+    if (ok) {
+      tmem_fence_after();
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const long long row = (long long)(qb + i) * a.H + h;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[32];
+        if (any) {
+          tmem_ld32_async(o_tm + 32 * c, o);
+          tmem_wait_ld32(o);
+        }
+        if (live) {
+          uint32_t w[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            w[k] = inv > 0.f ? pack_bf16x2(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv) : 0u;
+          uint4* dst = reinterpret_cast<uint4*>(a.out + row * C::D + 32 * c);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) dst[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+        }
+      }
+      if (live && a.lse) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    } else {
+      *abort_flag = 1;
+    }
+  }
+  tmem_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tmem_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+}
+
+}  // namespace pda
