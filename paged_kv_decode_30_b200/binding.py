@@ -426,24 +426,38 @@ def merge_states(o_parts, lse_parts, *, out=None, lse=None, sinks=None, stream=N
 
 
 def _check(name, t, dtype, shape, device, rows=False):
-    """Raise ValueError unless t is a CUDA tensor of this type and shape on
-    `device`, contiguous (``rows``: unit stride within a row is enough; None in
-    `shape` matches any size)."""
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if t.dtype != dtype:
+    """Raise ValueError unless t is a tensor of this type and shape on `device`,
+    contiguous (``rows``: unit stride within a row is enough)."""
+    if t.dtype is dtype and t.shape == shape and t.device == device and (
+            t.is_contiguous() or (rows and (t.shape[-1] <= 1 or t.stride(-1) == 1))):
+        return
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, not {t.device}")
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if not (t.is_contiguous() or (rows and (t.shape[-1] <= 1 or t.stride(-1) == 1))):
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _on_current_device(device):
-    """The library works on the current device: refuse tensors of another."""
+def _sizes(name, t, dims):
+    """The sizes of a tensor that must have `dims` dimensions."""
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, not {t.dim()}")
+    return t.shape
+
+
+def _current_stream(device, stream):
+    """The CUDA stream handle of a call on tensors of `device`: the given stream,
+    or the current one. The library works on the current device, so tensors of
+    another are refused."""
     import torch
     if device.type != "cuda" or device.index != torch.cuda.current_device():
         raise ValueError(f"the tensors are on {device}, which is not the current CUDA device")
+    if stream is not None:
+        return stream.cuda_stream or None
+    # (the handle itself: the Stream object around it costs two microseconds)
+    return torch._C._cuda_getCurrentRawStream(device.index) or None
 
 
 def _used_on(stream, *tensors):
@@ -461,38 +475,40 @@ def _row_stride(t):
 
 
 def _latent_pools(latent_pages, rope_pages, latent_scales, page_table):
-    """Check the pools of a latent cache and its page table; the KV dtype."""
+    """Check the pools of a latent cache and its page table. Returns their device,
+    (num_pages, page_size, latent_dim), rope_dim, (batch, max_pages) and KV dtype."""
     import torch
     dev = latent_pages.device
-    fp8 = latent_pages.dtype == torch.uint8
-    _check("latent_pages", latent_pages, torch.uint8 if fp8 else torch.bfloat16,
-           (None, None, None), dev)
-    pools = tuple(latent_pages.shape[:2])
-    _check("rope_pages", rope_pages, torch.bfloat16, pools + (None,), dev)
-    _check("page_table", page_table, torch.int32, (None, None), dev)
+    pools = _sizes("latent_pages", latent_pages, 3)
+    num_pages, page, _ = pools
+    rope_dim = _sizes("rope_pages", rope_pages, 3)[2]
+    table = _sizes("page_table", page_table, 2)
+    fp8 = latent_pages.dtype is torch.uint8
+    _check("latent_pages", latent_pages, torch.uint8 if fp8 else torch.bfloat16, pools, dev)
+    _check("rope_pages", rope_pages, torch.bfloat16, (num_pages, page, rope_dim), dev)
+    _check("page_table", page_table, torch.int32, table, dev)
     if fp8:
         if latent_scales is None:
             raise ValueError("uint8 latent_pages need latent_scales")
-        _check("latent_scales", latent_scales, torch.uint8, pools, dev)
+        _check("latent_scales", latent_scales, torch.uint8, (num_pages, page), dev)
     elif latent_scales is not None:
         raise ValueError("latent_scales go with uint8 latent_pages")
-    return PDA_KV_FP8_E4M3 if fp8 else PDA_KV_BF16
+    return dev, pools, rope_dim, table, PDA_KV_FP8_E4M3 if fp8 else PDA_KV_BF16
 
 
 def _latent_rows(latent, rope, row_offsets, page_table, starts, latent_pages, rope_pages,
                  latent_scales):
     import torch
-    kv_dtype = _latent_pools(latent_pages, rope_pages, latent_scales, page_table)
-    _on_current_device(latent_pages.device)
-    dev, (num_pages, page, width), batch = latent_pages.device, latent_pages.shape, page_table.shape[0]
-    rope_dim, rows = rope_pages.shape[2], latent.shape[0]
+    dev, (num_pages, page, width), rope_dim, (batch, max_pages), kv_dtype = _latent_pools(
+        latent_pages, rope_pages, latent_scales, page_table)
+    rows = _sizes("latent", latent, 2)[0]
     _check("latent", latent, torch.bfloat16, (rows, width), dev, rows=True)
     _check("rope", rope, torch.bfloat16, (rows, rope_dim), dev, rows=True)
     _check("row_offsets", row_offsets, torch.int32, (batch + 1,), dev)
     if starts is not None:
         _check("kv_lens / starts", starts, torch.int32, (batch,), dev)
-    return PdaLatentRowsParams(batch, rows, width, rope_dim, page, page_table.shape[1], num_pages,
-                               kv_dtype, _row_stride(latent), _row_stride(rope), _ptr(latent_scales))
+    return PdaLatentRowsParams(batch, rows, width, rope_dim, page, max_pages, num_pages, kv_dtype,
+                               _row_stride(latent), _row_stride(rope), _ptr(latent_scales))
 
 
 def paged_latent_append(latent, rope, row_offsets, page_table, kv_lens, latent_pages, rope_pages,
@@ -505,9 +521,10 @@ def paged_latent_append(latent, rope, row_offsets, page_table, kv_lens, latent_p
     power-of-two scale. latent and rope may be column slices of one tensor."""
     p = _latent_rows(latent, rope, row_offsets, page_table, kv_lens, latent_pages, rope_pages,
                      latent_scales)
-    st = load().paged_latent_append(_ptr(latent), _ptr(rope), _ptr(row_offsets), _ptr(page_table),
-                                    _ptr(kv_lens), ctypes.byref(p), _ptr(latent_pages),
-                                    _ptr(rope_pages), _stream_handle(stream))
+    st = load().paged_latent_append(latent.data_ptr(), rope.data_ptr(), row_offsets.data_ptr(),
+                                    page_table.data_ptr(), kv_lens.data_ptr(), p,
+                                    latent_pages.data_ptr(), rope_pages.data_ptr(),
+                                    _current_stream(latent.device, stream))
     if st != 0:
         raise PdaError(st, "paged_latent_append")
 
@@ -524,16 +541,17 @@ def paged_latent_gather(latent_pages, rope_pages, page_table, row_offsets, *, to
         if total_rows is None:
             raise ValueError("total_rows is needed to allocate the outputs")
         if latent is None:
-            latent = torch.empty((total_rows, latent_pages.shape[2]), dtype=torch.bfloat16,
-                                 device=latent_pages.device)
+            latent = torch.empty((total_rows, _sizes("latent_pages", latent_pages, 3)[2]),
+                                 dtype=torch.bfloat16, device=latent_pages.device)
         if rope is None:
-            rope = torch.empty((total_rows, rope_pages.shape[2]), dtype=torch.bfloat16,
-                               device=latent_pages.device)
+            rope = torch.empty((total_rows, _sizes("rope_pages", rope_pages, 3)[2]),
+                               dtype=torch.bfloat16, device=latent_pages.device)
     p = _latent_rows(latent, rope, row_offsets, page_table, starts, latent_pages, rope_pages,
                      latent_scales)
-    st = load().paged_latent_gather(_ptr(latent_pages), _ptr(rope_pages), _ptr(page_table),
-                                    _ptr(row_offsets), _ptr(starts), ctypes.byref(p), _ptr(latent),
-                                    _ptr(rope), _stream_handle(stream))
+    st = load().paged_latent_gather(latent_pages.data_ptr(), rope_pages.data_ptr(),
+                                    page_table.data_ptr(), row_offsets.data_ptr(), _ptr(starts), p,
+                                    latent.data_ptr(), rope.data_ptr(),
+                                    _current_stream(latent.device, stream))
     if st != 0:
         raise PdaError(st, "paged_latent_gather")
     _used_on(stream, latent, rope)
@@ -551,36 +569,34 @@ def paged_latent_decode(q, latent_pages, rope_pages, page_table, kv_lens, *, sca
     masks and workspace as for paged_decode_attn."""
     import torch
     lib = load()
-    kv_dtype = _latent_pools(latent_pages, rope_pages, latent_scales, page_table)
-    _on_current_device(q.device)
-    dev, (num_pages, page, width) = q.device, latent_pages.shape
-    rope_dim = rope_pages.shape[2]
-    _check("q", q, torch.bfloat16, (None, None, None, width + rope_dim), latent_pages.device)
-    B, q_len, H, _ = q.shape
-    _check("page_table", page_table, torch.int32, (B, None), dev)
+    dev, (num_pages, page, width), rope_dim, (B, max_pages), kv_dtype = _latent_pools(
+        latent_pages, rope_pages, latent_scales, page_table)
+    _, q_len, H, _ = _sizes("q", q, 4)
+    _check("q", q, torch.bfloat16, (B, q_len, H, width + rope_dim), dev)
     _check("kv_lens", kv_lens, torch.int32, (B,), dev)
+    handle = _current_stream(dev, stream)
     if out is None:
         out = torch.empty((B, q_len, H, width), dtype=torch.bfloat16, device=dev)
     else:
         _check("out", out, torch.bfloat16, (B, q_len, H, width), dev)
-    if lse is None and with_lse:
-        lse = torch.empty((B, q_len, H), dtype=torch.float32, device=dev)
-    elif lse is not None:
+    if lse is not None:
         _check("lse", lse, torch.float32, (B, q_len, H), dev)
-    p = PdaLatentParams(B, q_len, H, width, rope_dim, page, page_table.shape[1], num_pages, scale,
+    elif with_lse:
+        lse = torch.empty((B, q_len, H), dtype=torch.float32, device=dev)
+    p = PdaLatentParams(B, q_len, H, width, rope_dim, page, max_pages, num_pages, scale,
                         causal_offset, window, kv_dtype, flags, _ptr(latent_scales), None, 0)
     if workspace is None and not library_workspace:
-        need = lib.paged_latent_decode_workspace_bytes(ctypes.byref(p))
+        need = lib.paged_latent_decode_workspace_bytes(p)
         if need == ctypes.c_size_t(-1).value:
-            raise PdaError(1, "paged_latent_decode_workspace_bytes")
+            need = 0  # the call below says what is wrong
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     if workspace is not None:
         p.workspace = workspace.data_ptr()
-        p.workspace_bytes = workspace.numel() * workspace.element_size()
-    st = lib.paged_latent_decode(_ptr(q), _ptr(latent_pages), _ptr(rope_pages), _ptr(page_table),
-                                 _ptr(kv_lens), ctypes.byref(p), _ptr(out), _ptr(lse),
-                                 _stream_handle(stream))
+        p.workspace_bytes = workspace.nbytes
+    st = lib.paged_latent_decode(q.data_ptr(), latent_pages.data_ptr(), rope_pages.data_ptr(),
+                                 page_table.data_ptr(), kv_lens.data_ptr(), p, out.data_ptr(),
+                                 _ptr(lse), handle)
     if st != 0:
         raise PdaError(st, "paged_latent_decode")
     _used_on(stream, out, lse, workspace)
@@ -599,28 +615,28 @@ def latent_prefill_attn(q, kv, k_rope, q_offsets, kv_offsets, *, scale,
     import torch
     lib = load()
     dev = q.device
-    _on_current_device(dev)
-    _check("q", q, torch.bfloat16, (None, None, None), dev)
-    total_q, H, width = q.shape
-    _check("kv", kv, torch.bfloat16, (None, H, None), dev)
-    total_kv, D = kv.shape[0], kv.shape[2] // 2
-    _check("kv", kv, torch.bfloat16, (None, H, 2 * D), dev)
+    total_q, H, width = _sizes("q", q, 3)
+    total_kv, _, D2 = _sizes("kv", kv, 3)
+    D = D2 // 2
+    B = _sizes("q_offsets", q_offsets, 1)[0] - 1
+    _check("q", q, torch.bfloat16, (total_q, H, width), dev)
+    _check("kv", kv, torch.bfloat16, (total_kv, H, 2 * D), dev)
     _check("k_rope", k_rope, torch.bfloat16, (total_kv, width - D), dev, rows=True)
-    _check("q_offsets", q_offsets, torch.int32, (None,), dev)
-    B = q_offsets.shape[0] - 1
+    _check("q_offsets", q_offsets, torch.int32, (B + 1,), dev)
     _check("kv_offsets", kv_offsets, torch.int32, (B + 1,), dev)
+    handle = _current_stream(dev, stream)
     if out is None:
         out = torch.empty((total_q, H, D), dtype=torch.bfloat16, device=dev)
     else:
         _check("out", out, torch.bfloat16, (total_q, H, D), dev)
-    if lse is None and with_lse:
-        lse = torch.empty((total_q, H), dtype=torch.float32, device=dev)
-    elif lse is not None:
+    if lse is not None:
         _check("lse", lse, torch.float32, (total_q, H), dev)
+    elif with_lse:
+        lse = torch.empty((total_q, H), dtype=torch.float32, device=dev)
     p = PdaLatentPrefillParams(B, total_q, total_kv, total_q if max_q_len is None else max_q_len, H,
                                D, width - D, _row_stride(k_rope), scale, causal_offset, window)
-    st = lib.latent_prefill_attn(_ptr(q), _ptr(kv), _ptr(k_rope), _ptr(q_offsets), _ptr(kv_offsets),
-                                 ctypes.byref(p), _ptr(out), _ptr(lse), _stream_handle(stream))
+    st = lib.latent_prefill_attn(q.data_ptr(), kv.data_ptr(), k_rope.data_ptr(), q_offsets.data_ptr(),
+                                 kv_offsets.data_ptr(), p, out.data_ptr(), _ptr(lse), handle)
     if st != 0:
         raise PdaError(st, "latent_prefill_attn")
     _used_on(stream, out, lse)

@@ -15,7 +15,9 @@
 
 namespace pda {
 
-int* device_error_word();  // paged_decode_attn.cu
+// paged_decode_attn.cu
+int* device_error_word();
+int device_sms();
 
 namespace {
 
@@ -241,10 +243,8 @@ pda_status rows_call(const pda_latent_rows_params* p, bool write, void* latent, 
   if (!al(latent, 16) || !al(rope, 16) || !al(latent_pages, 16) || !al(rope_pages, 16) ||
       !al(row_offsets, 4) || !al(page_table, 4) || !al(starts, 4))
     return PDA_ERR_MISALIGNED;
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return PDA_ERR_CUDA;
+  const int sms = device_sms();
+  if (sms < 1) return PDA_ERR_CUDA;
   RowsArgs a{};
   a.row_offsets = row_offsets;
   a.page_table = page_table;
