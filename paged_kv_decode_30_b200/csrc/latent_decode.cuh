@@ -32,8 +32,9 @@
 // x + e, split in two e4m3 terms as well; the normaliser adds w_j 2^-e_j.
 //
 // Roles (warps): 0 TMA producer, 1 S^T issuer, 2 O^T issuer, 3 schedule,
-// 4.. softmax (NT / 16 groups of four warps, 16 rows a thread, thread = token
-// of S^T = element of an O^T block). Every wait is bounded.
+// 4.. softmax (groups of four warps, a thread = a token of S^T = an element of
+// each O^T block, with 8 query rows, 16 where 8 would take too many warps).
+// Every wait is bounded.
 #pragma once
 
 #include "pda_device.cuh"
@@ -150,7 +151,8 @@ struct LatentCfg {
   static constexpr int OFF_MISC = OFF_BAR + BARS * 8;   // TMEM address, abort flag, scan sums
   static constexpr int SMEM = OFF_MISC + 16 + 32 * 4;
   static constexpr int SMEM_ALLOC = SMEM + 1024;
-  static constexpr int GROUPS = NT / 16;
+  static constexpr int RH = NT == 64 ? 16 : 8;          // query rows per softmax thread
+  static constexpr int GROUPS = NT / RH;
   static constexpr int SOFT = 4;                        // first softmax warp
   static constexpr int WARPS = SOFT + 4 * GROUPS;
   static constexpr int THREADS = 32 * WARPS;
@@ -170,19 +172,34 @@ __device__ __forceinline__ uint32_t sw128(int n, int c) {
   return (n >> 3) * 1024 + (n & 7) * 128 + ((c ^ (n & 7)) << 4);
 }
 
-// Sums of 16 values over a warp's lanes: every step hands half of the values
-// to the partner, so lane l ends with the sum of value l / 2 in v[0].
-__device__ __forceinline__ void lane_sums(float (&v)[16], int lane) {
+// Sums of N values over a warp's lanes: every step hands half of the values to
+// the partner, so lane l ends with the sum of value l / (32 / N) in v[0].
+template <int N>
+__device__ __forceinline__ void lane_sums(float (&v)[N], int lane) {
+  int o = 16;
 #pragma unroll
-  for (int h = 8; h >= 1; h >>= 1) {
-    const bool up = lane & (2 * h);
+  for (int h = N / 2; h >= 1; h >>= 1, o >>= 1) {
+    const bool up = lane & o;
 #pragma unroll
     for (int k = 0; k < h; ++k) {
       const float send = up ? v[k] : v[k + h], keep = up ? v[k + h] : v[k];
-      v[k] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, 2 * h);
+      v[k] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, o);
     }
   }
-  v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], 1);
+#pragma unroll
+  for (; o >= 1; o >>= 1) v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
+}
+
+// N (8 or 16) consecutive fp32 TMEM columns of this thread's lane.
+template <int N>
+__device__ __forceinline__ void tmem_ldn(uint32_t taddr, float (&v)[N]) {
+  if constexpr (N == 16) tmem_ld16(taddr, v);
+  else tmem_ld8(taddr, v);
+}
+template <int N>
+__device__ __forceinline__ void tmem_stn(uint32_t taddr, const float (&v)[N]) {
+  if constexpr (N == 16) tmem_st16(taddr, v);
+  else tmem_st8(taddr, v);
 }
 
 template <int R, bool FP8, int NT>
@@ -537,11 +554,11 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
     __syncwarp();
   } else {
     // ======================= softmax ===========================================
-    // A group of four warps owns 16 query rows; thread i is token i of the tile
+    // A group of four warps owns RH query rows; thread i is token i of the tile
     // in S^T and element i of each block in O^T.
-    constexpr int GT = 128;
+    constexpr int GT = 128, RH = C::RH;
     constexpr float kLn2 = 0.69314718055994531f, kUnset = -1e30f;
-    const int q4 = warp & 3, grp = (warp - C::SOFT) >> 2, gbar = 2 + grp, r0 = 16 * grp;
+    const int q4 = warp & 3, grp = (warp - C::SOFT) >> 2, gbar = 2 + grp, r0 = RH * grp;
     const int i = 32 * q4 + lane;
     const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
     float* sm_m = reinterpret_cast<float*>(smem + C::OFF_M);
@@ -553,6 +570,7 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
     int2* sm_range = reinterpret_cast<int2*>(smem + C::OFF_RANGE);
     const uint32_t s_tm = tmem + lane_off + C::COL_S + (FP8 ? 2 * r0 : r0);
     const uint32_t o_tm = tmem + lane_off + C::COL_O + (FP8 ? 2 * r0 : r0);
+    const int R0 = rt * NT + r0, rows = min(RH, a.M - R0);  // this group's packed rows
     int g = 0;
     bool ok = true;
     for (int j = 0; ok; ++j) {
@@ -564,35 +582,31 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
       const LatentItem& d = items[j % C::ITEMS];
       if (d.b < 0) break;
       const int first = d.first, n = d.n, L = d.L, b = d.b;
-      const int R0 = rt * NT + r0;  // this group's first packed row
-      if (i < 16) {
-        int lo = 0, hi = 0;
-        if (R0 + i < a.M) latent_visible(a, L, (R0 + i) / a.H, lo, hi);
-        sm_range[r0 + i] = make_int2(lo, hi);
-        sm_m[r0 + i] = kUnset;
-      }
       if constexpr (FP8) {
         // The item's Q operand. 2^e2 puts a row's max |q_c| in [128, 256); then
         // q_c * 2^e2 = hi + lo / 16 in e4m3, exact for every element within
-        // 2^13 of the row's largest (others to 2^-21 of it).
-        if (j >= 1 && !mbar_wait(q_free, (j - 1) & 1, a.err)) *abort_flag = 1;
+        // 2^13 of the row's largest (others to 2^-21 of it). A warp has RH / 4
+        // rows; all their loads go out first.
         uint8_t* qs = smem + C::OFF_Q;
-        constexpr int E = R / 32;  // elements of a row per lane
-#pragma unroll 1
-        for (int rr = q4; rr < 16; rr += 4) {
-          const int nrow = r0 + rr, row = rt * NT + nrow;
+        constexpr int E = R / 32, W = RH / 4;  // elements of a row per lane, rows
+        uint4 raw[W][E / 8], rope[W];
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const int row = R0 + q4 + 4 * w;
+          const uint16_t* src = a.q + ((long long)b * a.M + row) * (R + a.rope_dim);
+#pragma unroll
+          for (int k = 0; k < E / 8; ++k)
+            raw[w][k] = row < a.M ? __ldg(reinterpret_cast<const uint4*>(src + lane * E) + k) : make_uint4(0, 0, 0, 0);
+          rope[w] = row < a.M && lane * 8 < a.rope_dim ? __ldg(reinterpret_cast<const uint4*>(src + R) + lane)
+                                                       : make_uint4(0, 0, 0, 0);
+        }
+        if (j >= 1 && !wait_or_abort(q_free, (j - 1) & 1, abort_flag, a.err)) *abort_flag = 1;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const int rr = q4 + 4 * w, nrow = r0 + rr;
           float f[E];
-          uint4 rope = make_uint4(0, 0, 0, 0);
 #pragma unroll
-          for (int k = 0; k < E; ++k) f[k] = 0.f;
-          if (row < a.M) {
-            const uint16_t* src = a.q + ((long long)b * a.M + row) * (R + a.rope_dim);
-#pragma unroll
-            for (int k = 0; k < E / 8; ++k)
-              bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(src + lane * E + 8 * k)),
-                            *reinterpret_cast<float(*)[8]>(f + 8 * k));
-            if (lane * 8 < a.rope_dim) rope = __ldg(reinterpret_cast<const uint4*>(src + R + lane * 8));
-          }
+          for (int k = 0; k < E / 8; ++k) bf16x8_to_f32(raw[w][k], *reinterpret_cast<float(*)[8]>(f + 8 * k));
           float mx = 0.f;
 #pragma unroll
           for (int k = 0; k < E; ++k) mx = fmaxf(mx, fabsf(f[k]));
@@ -602,17 +616,17 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
           if (lane == 0) sm_cs[nrow] = ldexpf(a.scale_log2, -e2);
           uint32_t hw[E / 4], lw[E / 4];
 #pragma unroll
-          for (int w = 0; w < E / 4; ++w) {
-            hw[w] = lw[w] = 0;
+          for (int x = 0; x < E / 4; ++x) {
+            hw[x] = lw[x] = 0;
 #pragma unroll
             for (int k = 0; k < 4; k += 2) {
-              const float x0 = f[4 * w + k] * up, x1 = f[4 * w + k + 1] * up;
+              const float x0 = f[4 * x + k] * up, x1 = f[4 * x + k + 1] * up;
               const uint32_t h2 = f32x2_to_e4m3x2(x0, x1);
-              hw[w] |= h2 << (8 * k);
-              lw[w] |= f32x2_to_e4m3x2((x0 - e4m3_to_f32(h2)) * 16.f, (x1 - e4m3_to_f32(h2 >> 8)) * 16.f) << (8 * k);
+              hw[x] |= h2 << (8 * k);
+              lw[x] |= f32x2_to_e4m3x2((x0 - e4m3_to_f32(h2)) * 16.f, (x1 - e4m3_to_f32(h2 >> 8)) * 16.f) << (8 * k);
             }
           }
-          const int rh = 2 * r0 + rr, rl = rh + 16, el = lane * E;
+          const int rh = 2 * r0 + rr, rl = rh + RH, el = lane * E;
           uint8_t* blk_base = qs + (el >> 7) * C::Q_BLK;
           const int c = (el & 127) >> 4;
           if constexpr (E == 16) {
@@ -622,10 +636,16 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
             *reinterpret_cast<uint2*>(blk_base + sw128(rh, c) + (el & 8)) = make_uint2(hw[0], hw[1]);
             *reinterpret_cast<uint2*>(blk_base + sw128(rl, c) + (el & 8)) = make_uint2(lw[0], lw[1]);
           }
-          if (lane < 8) *reinterpret_cast<uint4*>(qs + C::Q_ROPE + sw128(nrow, lane)) = rope;
+          if (lane < 8) *reinterpret_cast<uint4*>(qs + C::Q_ROPE + sw128(nrow, lane)) = rope[w];
         }
         fence_proxy_async_smem();
         mbar_arrive(q_full);
+      }
+      if (i < RH) {
+        int lo = 0, hi = 0;
+        if (R0 + i < a.M) latent_visible(a, L, (R0 + i) / a.H, lo, hi);
+        sm_range[r0 + i] = make_int2(lo, hi);
+        sm_m[r0 + i] = kUnset;
       }
       named_bar(gbar, GT);
       // FP8: this token's scale exponent, looked up a tile ahead
@@ -638,41 +658,39 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
         return __ldg(a.scales + (long long)page * a.page_size + (jt & (a.page_size - 1)));
       };
       int sc_next = scale_of(first);
-      float l_sum[16], l_rnd[16];  // this token's part of the row sums: of the weights, of the rounded ones
+      float l_sum[RH], l_rnd[RH];  // this token's part of the row sums: of the weights, of the rounded ones
 #pragma unroll
-      for (int r = 0; r < 16; ++r) l_sum[r] = l_rnd[r] = 0.f;
+      for (int r = 0; r < RH; ++r) l_sum[r] = l_rnd[r] = 0.f;
       for (int t = first; t < first + n; ++t, ++g) {
         const int bb = g & 1;
         const float e_tok = FP8 ? (float)(min(max(sc_next, 97), 157) - 127) : 0.f;
         sc_next = scale_of(t + 1);
         bool good = __all_sync(FULL, wait_or_abort(&s_full[bb], (g >> 1) & 1, abort_flag, a.err));
-        float x[16];
+        float x[RH];
         if (good) {
           tmem_fence_after();
           const uint32_t ta = s_tm + bb * C::SN;
           if constexpr (FP8) {
             const float up = __int_as_float((int)(e_tok + 127.f) << 23);
-            float y[16];
-            tmem_ld16(ta, x);
-            tmem_ld16(ta + 16, y);
+            float hl[2 * RH], y[RH];
+            tmem_ldn(ta, hl);
+            tmem_ldn(tmem + lane_off + C::COL_S + bb * C::SN + C::N1 + r0, y);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) x[r] = fmaf(y[r], 0.0625f, x[r]) * up * sm_cs[r0 + r];
-            tmem_ld16(tmem + lane_off + C::COL_S + bb * C::SN + C::N1 + r0, y);
-#pragma unroll
-            for (int r = 0; r < 16; ++r) x[r] = fmaf(y[r], a.scale_log2, x[r]) + e_tok;
+            for (int r = 0; r < RH; ++r)
+              x[r] = fmaf(y[r], a.scale_log2, fmaf(hl[RH + r], 0.0625f, hl[r]) * up * sm_cs[r0 + r]) + e_tok;
           } else {
-            tmem_ld16(ta, x);
+            tmem_ldn(ta, x);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) x[r] *= a.scale_log2;
+            for (int r = 0; r < RH; ++r) x[r] *= a.scale_log2;
           }
         } else {
 #pragma unroll
-          for (int r = 0; r < 16; ++r) x[r] = -INFINITY;
+          for (int r = 0; r < RH; ++r) x[r] = -INFINITY;
         }
         const int t0 = t * kTile, jt = t0 + i;
         if (!(t0 >= d.lo_x && t0 + kTile <= d.hi_x)) {
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
+          for (int r = 0; r < RH; ++r) {
             const int2 v = sm_range[r0 + r];
             if (!(jt >= v.x && jt < v.y)) x[r] = -INFINITY;
           }
@@ -694,7 +712,7 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
         // a weight would pass 2^8; most tiles skip the exchange.
         bool want = !good;
 #pragma unroll
-        for (int r = 0; r < 16; r += 4) {
+        for (int r = 0; r < RH; r += 4) {
           const float4 m = reinterpret_cast<const float4*>(sm_m + r0)[r / 4];
           want |= (x[r] - m.x > 8.f) | (x[r + 1] - m.y > 8.f) | (x[r + 2] - m.z > 8.f) | (x[r + 3] - m.w > 8.f);
         }
@@ -704,12 +722,12 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
             break;
           }
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
+          for (int r = 0; r < RH; ++r) {
             const float wm = redux_max(x[r]);
             if (lane == r) wmax[q4 * NT + r0 + r] = wm;
           }
           named_bar(gbar, GT);
-          if (i < 16) {
+          if (i < RH) {
             const int rr = r0 + i;
             const float top = fmaxf(fmaxf(wmax[rr], wmax[NT + rr]), fmaxf(wmax[2 * NT + rr], wmax[3 * NT + rr]));
             const float m_old = sm_m[rr], m_new = fmaxf(m_old, top - C::HEAD);
@@ -717,24 +735,25 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
             sm_m[rr] = m_new;
           }
           named_bar(gbar, GT);
-          const float* al = sm_alpha + r0;
+          float al[RH];
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
+          for (int r = 0; r < RH; ++r) {
+            al[r] = sm_alpha[r0 + r];
             l_sum[r] *= al[r];
             l_rnd[r] *= al[r];
           }
           if (t > first) {  // what the item's earlier tiles added moves along
-            good = __all_sync(FULL, mbar_wait(&o_full[(g - 1) & 1], ((g - 1) >> 1) & 1, a.err));
+            good = __all_sync(FULL, wait_or_abort(&o_full[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag, a.err));
             if (good) {
               tmem_fence_after();
 #pragma unroll 1
               for (int k = 0; k < C::NB * (FP8 ? 2 : 1); ++k) {
-                const uint32_t ta = o_tm + (FP8 ? (k >> 1) * C::N2 + (k & 1) * 16 : k * C::N2);
-                float o[16];
-                tmem_ld16(ta, o);
+                const uint32_t ta = o_tm + (FP8 ? (k >> 1) * C::N2 + (k & 1) * RH : k * C::N2);
+                float o[RH];
+                tmem_ldn(ta, o);
 #pragma unroll
-                for (int r = 0; r < 16; ++r) o[r] *= al[r];
-                tmem_st16(ta, o);
+                for (int r = 0; r < RH; ++r) o[r] *= al[r];
+                tmem_stn(ta, o);
               }
               tmem_fence_before();
             } else {
@@ -742,69 +761,70 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
             }
           }
         }
-        const float down = FP8 ? __int_as_float((int)(127.f - e_tok) << 23) : 1.f;
 #pragma unroll
-        for (int r = 0; r < 16; r += 4) {
+        for (int r = 0; r < RH; r += 4) {
           const float4 m = reinterpret_cast<const float4*>(sm_m + r0)[r / 4];
           x[r] = fast_exp2(x[r] - m.x);
           x[r + 1] = fast_exp2(x[r + 1] - m.y);
           x[r + 2] = fast_exp2(x[r + 2] - m.z);
           x[r + 3] = fast_exp2(x[r + 3] - m.w);
         }
-        uint32_t w[8];
+        uint32_t w[RH / 2];  // FP8: first terms, then second terms; bf16: pairs
         if constexpr (FP8) {
 #pragma unroll
-          for (int r = 0; r < 16; r += 4) {
+          for (int r = 0; r < RH; r += 4) {
             const uint32_t s01 = e4m3_split2(x[r], x[r + 1]), s23 = e4m3_split2(x[r + 2], x[r + 3]);
             w[r / 4] = __byte_perm(s01, s23, 0x5410);
-            w[4 + r / 4] = __byte_perm(s01, s23, 0x7632);
+            w[RH / 4 + r / 4] = __byte_perm(s01, s23, 0x7632);
           }
-#pragma unroll
-          for (int r = 0; r < 16; ++r) l_sum[r] = fmaf(x[r], down, l_sum[r]);
         } else {
 #pragma unroll
-          for (int r = 0; r < 16; r += 2) {
-            w[r / 2] = pack_bf16x2(x[r], x[r + 1]);
+          for (int r = 0; r < RH; r += 2) w[r / 2] = pack_bf16x2(x[r], x[r + 1]);
+        }
+        // The buffer's last reader: the O^T products P_BUFS tiles ago. (Overlay:
+        // the rotated parts of this tile were loaded after those, and read.)
+        if (!C::OVERLAY && g >= C::P_BUFS) {
+          const int u = g - C::P_BUFS;
+          if (!wait_or_abort(&o_full[u & 1], (u >> 1) & 1, abort_flag, a.err)) *abort_flag = 1;
+        }
+        uint8_t* sp = smem + C::OFF_P + (g % C::P_BUFS) * C::P_BYTES + i * C::P_ROW;
+        const int z = C::P_ROW == 128 ? i & 7 : C::P_ROW == 64 ? (i >> 1) & 3 : (i >> 2) & 1;
+#pragma unroll
+        for (int c = 0; c < RH / 8; ++c)
+          *reinterpret_cast<uint4*>(sp + (((RH / 8 * grp + c) ^ z) << 4)) =
+              make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+        fence_proxy_async_smem();
+        tmem_fence_before();
+        mbar_arrive(&p_ready[bb]);
+        // the sums, beside the products
+        if constexpr (FP8) {
+          const float down = __int_as_float((int)(127.f - e_tok) << 23);
+#pragma unroll
+          for (int r = 0; r < RH; ++r) l_sum[r] = fmaf(x[r], down, l_sum[r]);
+        } else {
+#pragma unroll
+          for (int r = 0; r < RH; r += 2) {
             l_sum[r] += x[r];
             l_sum[r + 1] += x[r + 1];
             l_rnd[r] += __uint_as_float(w[r / 2] << 16);
             l_rnd[r + 1] += __uint_as_float(w[r / 2] & 0xFFFF0000u);
           }
         }
-        // The buffer's last reader: the O^T products P_BUFS tiles ago. (Overlay:
-        // the rotated parts of this tile were loaded after those, and read.)
-        if (!C::OVERLAY && g >= C::P_BUFS) {
-          const int u = g - C::P_BUFS;
-          if (!mbar_wait(&o_full[u & 1], (u >> 1) & 1, a.err)) *abort_flag = 1;
-        }
-        uint8_t* sp = smem + C::OFF_P + (g % C::P_BUFS) * C::P_BYTES + i * C::P_ROW;
-        const int z = C::P_ROW == 128 ? i & 7 : C::P_ROW == 64 ? (i >> 1) & 3 : (i >> 2) & 1;
-        *reinterpret_cast<uint4*>(sp + (((2 * grp) ^ z) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4*>(sp + (((2 * grp + 1) ^ z) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
-        fence_proxy_async_smem();
-        tmem_fence_before();
-        mbar_arrive(&p_ready[bb]);
       }
       if (!ok) break;
-      // ---- the item's end: normalise O^T and store it, or the partial results
-      bool good = true;
-      if (n > 0) good = mbar_wait(&o_full[(g - 1) & 1], ((g - 1) >> 1) & 1, a.err);
-      if (!named_bar_and(gbar, GT, good && !*abort_flag)) {
-        ok = false;
-        break;
-      }
-      tmem_fence_after();
-      // sums over the 128 tokens, in one order: over the warp's lanes, each
-      // lane ending with one row's sum, then over the four warps
+      // ---- the item's end: normalise O^T and store it, or the partial results.
+      // Sums over the 128 tokens in one order, over the warp's lanes, each lane
+      // ending with one row's sum, then over the four warps; beside the last
+      // tile's products.
       lane_sums(l_sum, lane);
       if constexpr (!FP8) lane_sums(l_rnd, lane);
-      if ((lane & 1) == 0) {
-        lred[q4 * NT + r0 + (lane >> 1)] = l_sum[0];
-        if constexpr (!FP8) lred[(4 + q4) * NT + r0 + (lane >> 1)] = l_rnd[0];
+      if (lane % (32 / RH) == 0) {
+        lred[q4 * NT + r0 + lane / (32 / RH)] = l_sum[0];
+        if constexpr (!FP8) lred[(4 + q4) * NT + r0 + lane / (32 / RH)] = l_rnd[0];
       }
       named_bar(gbar, GT);
-      const int part = d.part, rows = min(16, a.M - R0);
-      if (i < 16) {
+      const int part = d.part;
+      if (i < RH) {
         const int rr = r0 + i;
         const float l = lred[rr] + lred[NT + rr] + lred[2 * NT + rr] + lred[3 * NT + rr];
         const float ln = FP8 ? l : lred[4 * NT + rr] + lred[5 * NT + rr] + lred[6 * NT + rr] + lred[7 * NT + rr];
@@ -816,41 +836,49 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
         sm_inv[rr] = ln > 0.f ? 1.f / ln : 0.f;
       }
       named_bar(gbar, GT);
-      float inv[16];
+      float inv[RH];
 #pragma unroll
-      for (int r = 0; r < 16; ++r) inv[r] = sm_inv[r0 + r];
+      for (int r = 0; r < RH; ++r) inv[r] = sm_inv[r0 + r];
       float* po = a.o_part + ((long long)part * NT + r0) * R + i;
       uint16_t* oo = a.out + ((long long)b * a.M + R0) * R + i;
+      bool good = true;
 #pragma unroll (NT == 64 ? 1 : 2)
       for (int k = 0; k < C::NB; ++k, po += 128, oo += 128) {
-        float o[16];
-        if (n > 0) {
-          tmem_ld16(o_tm + k * C::N2, o);
-          if constexpr (FP8) {
-            float lo[16];
-            tmem_ld16(o_tm + k * C::N2 + 16, lo);
+        float o[RH];
 #pragma unroll
-            for (int r = 0; r < 16; ++r) o[r] = fmaf(lo[r], 0.0625f, o[r]);
+        for (int r = 0; r < RH; ++r) o[r] = 0.f;
+        if (n > 0) {  // block k of the last tile has been added
+          const int blk = (g - 1) * C::NB + k;
+          good = good && wait_or_abort(&empty[blk % C::SLOTS], (blk / C::SLOTS) & 1, abort_flag, a.err);
+          if (!__all_sync(FULL, good)) break;
+          tmem_fence_after();
+          if constexpr (FP8) {
+            float hl[2 * RH];
+            tmem_ldn(o_tm + k * C::N2, hl);
+#pragma unroll
+            for (int r = 0; r < RH; ++r) o[r] = fmaf(hl[RH + r], 0.0625f, hl[r]);
+          } else {
+            tmem_ldn(o_tm + k * C::N2, o);
           }
 #pragma unroll
-          for (int r = 0; r < 16; ++r) o[r] = inv[r] > 0.f ? o[r] * inv[r] : 0.f;
-        } else {
-#pragma unroll
-          for (int r = 0; r < 16; ++r) o[r] = 0.f;
+          for (int r = 0; r < RH; ++r) o[r] = inv[r] > 0.f ? o[r] * inv[r] : 0.f;
         }
         if (part >= 0) {
 #pragma unroll
-          for (int r = 0; r < 16; ++r)
+          for (int r = 0; r < RH; ++r)
             if (r < rows) po[r * R] = o[r];
         } else {
 #pragma unroll
-          for (int r = 0; r < 16; ++r)
+          for (int r = 0; r < RH; ++r)
             if (r < rows) oo[r * R] = __bfloat16_as_ushort(__float2bfloat16_rn(o[r]));
         }
       }
       tmem_fence_before();
       mbar_arrive(o_free);
-      named_bar(gbar, GT);  // the group no longer reads the item and its row state
+      if (!named_bar_and(gbar, GT, good)) {  // the group no longer reads the item and its row state
+        ok = false;
+        break;
+      }
       if (i == 0) mbar_arrive(&item_free[j % C::ITEMS]);
     }
     if (!ok) *abort_flag = 1;
