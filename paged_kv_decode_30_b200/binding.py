@@ -12,6 +12,8 @@ import ctypes
 import os
 from typing import Optional
 
+import torch
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libpaged_decode_attn.so")
 
@@ -429,7 +431,7 @@ def _check(name, t, dtype, shape, device, rows=False):
     """Raise ValueError unless t is a tensor of this type and shape on `device`,
     contiguous (``rows``: unit stride within a row is enough)."""
     if t.dtype is dtype and t.shape == shape and t.device == device and (
-            t.is_contiguous() or (rows and (t.shape[-1] <= 1 or t.stride(-1) == 1))):
+            t.is_contiguous() or (rows and t.stride(-1) == 1)):
         return
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, not {t.device}")
@@ -451,7 +453,6 @@ def _current_stream(device, stream):
     """The CUDA stream handle of a call on tensors of `device`: the given stream,
     or the current one. The library works on the current device, so tensors of
     another are refused."""
-    import torch
     if device.type != "cuda" or device.index != torch.cuda.current_device():
         raise ValueError(f"the tensors are on {device}, which is not the current CUDA device")
     if stream is not None:
@@ -477,7 +478,6 @@ def _row_stride(t):
 def _latent_pools(latent_pages, rope_pages, latent_scales, page_table):
     """Check the pools of a latent cache and its page table. Returns their device,
     (num_pages, page_size, latent_dim), rope_dim, (batch, max_pages) and KV dtype."""
-    import torch
     dev = latent_pages.device
     pools = _sizes("latent_pages", latent_pages, 3)
     num_pages, page, _ = pools
@@ -498,7 +498,6 @@ def _latent_pools(latent_pages, rope_pages, latent_scales, page_table):
 
 def _latent_rows(latent, rope, row_offsets, page_table, starts, latent_pages, rope_pages,
                  latent_scales):
-    import torch
     dev, (num_pages, page, width), rope_dim, (batch, max_pages), kv_dtype = _latent_pools(
         latent_pages, rope_pages, latent_scales, page_table)
     rows = _sizes("latent", latent, 2)[0]
@@ -536,7 +535,6 @@ def paged_latent_gather(latent_pages, rope_pages, page_table, row_offsets, *, to
     row_offsets[b + 1] of the outputs. Returns (latent [rows, R], rope [rows,
     Dr]): the given ones (rows behind row_offsets[B] are left alone), or new
     ones of total_rows rows."""
-    import torch
     if latent is None or rope is None:
         if total_rows is None:
             raise ValueError("total_rows is needed to allocate the outputs")
@@ -567,7 +565,6 @@ def paged_latent_decode(q, latent_pages, rope_pages, page_table, kv_lens, *, sca
     the latents and its rotated part; out bf16 [B, q_len, H, R] is the weighted
     sum of latents, lse fp32 [B, q_len, H]. Pools as for paged_latent_append;
     masks and workspace as for paged_decode_attn."""
-    import torch
     lib = load()
     dev, (num_pages, page, width), rope_dim, (B, max_pages), kv_dtype = _latent_pools(
         latent_pages, rope_pages, latent_scales, page_table)
@@ -612,7 +609,6 @@ def latent_prefill_attn(q, kv, k_rope, q_offsets, kv_offsets, *, scale,
     shared by the heads; q_offsets, kv_offsets int32 [B + 1]. ``max_q_len``:
     a bound on the query rows of a sequence (default total_q; a tighter one
     launches fewer idle CTAs). out bf16 [total_q, H, D], lse fp32 [total_q, H]."""
-    import torch
     lib = load()
     dev = q.device
     total_q, H, width = _sizes("q", q, 3)
