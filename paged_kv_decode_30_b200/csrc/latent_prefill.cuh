@@ -21,10 +21,10 @@
 // Shared memory: Q 96 KB, two stages of K (48 KB each) and one V (32 KB, freed
 // and filled in halves of 64 keys). No room for a second V.
 //
-// Roles (warps): 0 TMA producer, 1 MMA issuer (which also zeroes the V rows
-// that no query row sees: they may hold NaN, which a zero weight does not
-// cancel), 2-3 idle; 4-7 softmax of tile A, 8-11 of tile B, a thread a query
-// row. Every wait is bounded.
+// Roles (warps): 0 TMA producer, 1 and 2 MMA issuers of tiles A and B (which
+// also zero the V rows that no query row sees: they may hold NaN, which a zero
+// weight does not cancel), 3 idle; 4-7 softmax of tile A, 8-11 of tile B, a
+// thread a query row. Every wait is bounded.
 #pragma once
 
 #include "pda_device.cuh"
@@ -50,8 +50,8 @@ struct PrefillCfg {
   static constexpr int OFF_K = OFF_Q + 6 * CHUNK;    // 2 stages x 3 chunks
   static constexpr int OFF_V = OFF_K + 6 * CHUNK;    // 2 chunks
   static constexpr int OFF_BAR = OFF_V + 2 * CHUNK;
-  // q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2]
-  static constexpr int BARS = 16;
+  // q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2][2], o_full[2], turn[2]
+  static constexpr int BARS = 20;
   static constexpr int OFF_MISC = OFF_BAR + BARS * 8;
   static constexpr int SMEM_ALLOC = OFF_MISC + 16 + 1024;
   static constexpr int THREADS = 384;
@@ -127,6 +127,60 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// 2^x of two values in [-inf, 127) on the FMA pipe: x = n + f with n the nearest
+// integer (at least -125), 2^f = 1 + f q(f) on [-1/2, 1/2] with q of degree 4,
+// fitted for the least largest relative error (2^-23.1), 2^n added to the exponent.
+__device__ __forceinline__ void exp2_fma(f32x2 x, float& u, float& v) {
+  float a, b;
+  f2_unpack(x, a, b);
+  x = f2_pack(fmaxf(a, -125.f), fmaxf(b, -125.f));
+  const f32x2 magic = f2_pack(12582912.f, 12582912.f), back = f2_pack(-12582912.f, -12582912.f);
+  const f32x2 t = f2_add(x, magic);  // n in the low bits
+  const f32x2 n = f2_add(t, back);
+  const f32x2 f = f2_fma(n, f2_pack(-1.f, -1.f), x);
+  f32x2 q = f2_pack(0.001326472731307149f, 0.001326472731307149f);
+  q = f2_fma(q, f, f2_pack(0.009671512991189957f, 0.009671512991189957f));
+  q = f2_fma(q, f, f2_pack(0.05550733581185341f, 0.05550733581185341f));
+  q = f2_fma(q, f, f2_pack(0.24022242426872253f, 0.24022242426872253f));
+  q = f2_fma(q, f, f2_pack(0.6931470036506653f, 0.6931470036506653f));
+  q = f2_fma(q, f, f2_pack(1.f, 1.f));
+  float ru, rv, tu, tv;
+  f2_unpack(q, ru, rv);
+  f2_unpack(t, tu, tv);
+  u = __uint_as_float(__float_as_uint(ru) + (__float_as_uint(tu) << 23));
+  v = __uint_as_float(__float_as_uint(rv) + (__float_as_uint(tv) << 23));
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Weights 2^(s * scale - m) of 64 scores, as bf16 pairs, and their sum added to
+// `sum`. The special function units alone would take 8 cycles a warp and value;
+// MIX hands one pair in kMixEvery to the FMA pipe. Masked scores (-inf) want
+// exact zeros: no MIX.
+constexpr int kMixEvery = 4;
+template <bool MIX>
+__device__ __forceinline__ void weights64(const uint32_t* s, f32x2 scale2, f32x2 minus_m2, f32x2 (&sum)[2],
+                                          uint32_t* p) {
+#pragma unroll
+  for (int k = 0; k < 64; k += 2) {
+    const f32x2 x = f2_fma(f2_pack(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), scale2, minus_m2);
+    float u, v;
+    if (MIX && (k >> 1) % kMixEvery == kMixEvery - 1) {
+      exp2_fma(x, u, v);
+    } else {
+      f2_unpack(x, u, v);
+      u = fast_exp2(u);
+      v = fast_exp2(v);
+    }
+    sum[(k >> 1) & 1] = f2_add(sum[(k >> 1) & 1], f2_pack(u, v));
+    p[k >> 1] = pack_bf16x2(u, v);
+  }
+}
+
 __global__ void __launch_bounds__(PrefillCfg::THREADS, 1)
     latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_kv,
                           const __grid_constant__ CUtensorMap map_r, const PrefillArgs a) {
@@ -154,8 +208,9 @@ __global__ void __launch_bounds__(PrefillCfg::THREADS, 1)
   uint64_t* v_full = k_empty + 2;  // [half]
   uint64_t* v_empty = v_full + 2;  // [half]
   uint64_t* s_full = v_empty + 2;  // [tile] S in TMEM, and the products before it done
-  uint64_t* p_full = s_full + 2;   // [tile] weights in TMEM
-  uint64_t* o_full = p_full + 2;   // [tile] all products done
+  uint64_t* p_full = s_full + 2;   // [tile][half] weights of 64 keys in TMEM
+  uint64_t* o_full = p_full + 4;   // [tile] all products done
+  uint64_t* turn = o_full + 2;     // [tile] its products of a step may be issued
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
 
@@ -186,7 +241,8 @@ __global__ void __launch_bounds__(PrefillCfg::THREADS, 1)
 
   if (tid < C::BARS) {
     uint64_t* bar = q_full + tid;
-    mbar_init(bar, bar >= p_full && bar < o_full ? 128 : 1);
+    const bool both = (bar >= k_empty && bar < v_full) || (bar >= v_empty && bar < s_full);  // both MMA warps
+    mbar_init(bar, bar >= p_full && bar < o_full ? 128 : both ? 2 : 1);
     fence_mbar_init();
   }
   if (tid == 0) *abort_flag = 0;
@@ -258,17 +314,28 @@ __global__ void __launch_bounds__(PrefillCfg::THREADS, 1)
         }
       }
       __syncwarp();
-    } else if (warp == 1) {
-      // ======================= MMA issuer =======================================
+    } else if (warp < 3) {
+      // ======================= MMA issuers: tile A (warp 1), tile B (warp 2) =====
+      // A warp's issue runs only a few products ahead of the tensor core, so what
+      // it spends on barriers would leave the core idle: with a warp a tile, one
+      // looks at its barriers while the other's products run. Both follow every
+      // key tile, so that no barrier gets two phases ahead of either.
+      const int x = warp - 1;
       const bool leader = elect_one();
       bool ok = true;
-      int issued[2] = {0, 0};  // S products so far
+      int issued = 0;  // S products so far
       auto agreed = [&](bool v) { return __all_sync(FULL, v); };
-      auto scores = [&](int x, int t) {  // S_x = Q_x K(t)^T
+      auto scores = [&](int t) {  // S_x = Q_x K(t)^T, K(t) has landed
         const int st = (t - tb) & 1;
-        ok = ok && agreed(wait_or_abort(&k_full[st], ((t - tb) >> 1) & 1, abort_flag, a.err));
-        if (ok && t == t0[x]) ok = agreed(wait_or_abort(&q_full[x], 0, abort_flag, a.err));
-        if (!ok) return;
+        if (!active(x, t)) {
+          if (lane == 0) mbar_arrive(&k_empty[st]);
+          __syncwarp();
+          return;
+        }
+        if (t == t0[x]) {
+          ok = agreed(wait_or_abort(&q_full[x], 0, abort_flag, a.err));
+          if (!ok) return;
+        }
         tmem_fence_after();
         if (leader) {
           constexpr uint32_t idesc = umma_idesc_bf16(128, 128, false, false);
@@ -280,44 +347,30 @@ __global__ void __launch_bounds__(PrefillCfg::THREADS, 1)
             umma_f16(tmem + C::COL_S + x * 128, qd + off, kd + off, idesc, s > 0);
           }
           umma_commit(&s_full[x]);
+          umma_commit(&k_empty[st]);
         }
         __syncwarp();
-        ++issued[x];
+        ++issued;
       };
-      auto values = [&](int x, int t, bool last_reader) {  // O_x += P_x V(t)
-        ok = ok && agreed(wait_or_abort(&p_full[x], (t - t0[x]) & 1, abort_flag, a.err));
-        const uint64_t vd = umma_desc(sbase + C::OFF_V, C::CHUNK, 1024, kSw128);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          ok = ok && agreed(wait_or_abort(&v_full[half], (t - tb) & 1, abort_flag, a.err));
-          if (!ok) return;
-          tmem_fence_after();
-          if (leader) {
-            constexpr uint32_t idesc = umma_idesc_bf16(128, 128, false, true);
-#pragma unroll
-            for (int s = 4 * half; s < 4 * half + 4; ++s)
-              umma_f16_ts(tmem + C::COL_O + x * 128, tmem + C::COL_S + x * 128 + 8 * s, vd + ((s * 2048) >> 4),
-                          idesc, t > t0[x] || s > 0);
-            if (last_reader) umma_commit(&v_empty[half]);
-          }
-          __syncwarp();
-        }
-        if (t + 1 == t1[x]) {
-          if (leader) umma_commit(&o_full[x]);
-          __syncwarp();
-        }
+      auto key_tile = [&](int t) {
+        return agreed(wait_or_abort(&k_full[(t - tb) & 1], ((t - tb) >> 1) & 1, abort_flag, a.err));
+      };
+      // The tiles' products alternate step by step. Left alone the two drift into
+      // step, both with their softmax and then both with their products.
+      auto my_turn = [&](int n) {
+        return x == 0 && n == 0 ? true : agreed(wait_or_abort(&turn[x], (n - (x == 0 ? 1 : 0)) & 1, abort_flag, a.err));
       };
       if (te > tb) {
-        if (active(0, tb)) scores(0, tb);
-        if (active(1, tb)) scores(1, tb);
-        if (ok && leader) umma_commit(&k_empty[0]);
-        __syncwarp();
+        ok = key_tile(tb);
+        if (ok) scores(tb);
       }
       for (int t = tb; ok && t < te; ++t) {
-        if (ragged(t)) {  // V rows that no query row sees become zeros
-          ok = agreed(wait_or_abort(&v_full[0], (t - tb) & 1, abort_flag, a.err) &&
-                      wait_or_abort(&v_full[1], (t - tb) & 1, abort_flag, a.err));
-          if (!ok) break;
+        const int n = t - tb;
+        ok = (t + 1 == te || key_tile(t + 1)) &&
+             agreed(wait_or_abort(&v_full[0], n & 1, abort_flag, a.err) &&
+                    wait_or_abort(&v_full[1], n & 1, abort_flag, a.err));
+        if (!ok) break;
+        if (ragged(t)) {  // V rows that no query row sees become zeros; both warps write the same
           for (int r = lane; r < C::KT; r += 32) {
             const int key = t * C::KT + r;
             if (key >= lo_u && key < hi_u) continue;
@@ -332,20 +385,42 @@ __global__ void __launch_bounds__(PrefillCfg::THREADS, 1)
           fence_proxy_async_smem();
           __syncwarp();
         }
-        const bool next = t + 1 < te;
-        if (ok && active(0, t)) values(0, t, !active(1, t));
-        if (ok && next && active(0, t + 1)) scores(0, t + 1);
-        if (ok && active(1, t)) values(1, t, true);
-        if (ok && next && active(1, t + 1)) scores(1, t + 1);
-        if (ok && next && leader) umma_commit(&k_empty[(t + 1 - tb) & 1]);
+        if (active(x, t)) {  // O_x += P_x V(t), as the halves of P_x come
+          const uint64_t vd = umma_desc(sbase + C::OFF_V, C::CHUNK, 1024, kSw128);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            ok = ok && agreed(wait_or_abort(&p_full[2 * x + half], (t - t0[x]) & 1, abort_flag, a.err));
+            if (half == 0 && ok) ok = my_turn(n);
+            if (!ok) break;
+            tmem_fence_after();
+            if (leader) {
+              constexpr uint32_t idesc = umma_idesc_bf16(128, 128, false, true);
+#pragma unroll
+              for (int s = 4 * half; s < 4 * half + 4; ++s)
+                umma_f16_ts(tmem + C::COL_O + x * 128, tmem + C::COL_S + x * 128 + 8 * s, vd + ((s * 2048) >> 4),
+                            idesc, t > t0[x] || s > 0);
+              umma_commit(&v_empty[half]);
+              if (half == 1 && t + 1 == t1[x]) umma_commit(&o_full[x]);
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+        } else {
+          ok = my_turn(n);
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive(&v_empty[0]);
+            mbar_arrive(&v_empty[1]);
+          }
+          __syncwarp();
+        }
+        if (t + 1 < te) scores(t + 1);
+        if (lane == 0) mbar_arrive(&turn[1 - x]);
         __syncwarp();
       }
       if (!ok) *abort_flag = 1;
-      if (*abort_flag) {  // MMAs already issued finish before TMEM is freed
-        if (leader) umma_commit(&v_empty[0]);
-        for (int x = 0; x < 2; ++x)
-          if (issued[x] > 0) mbar_wait(&s_full[x], (issued[x] - 1) & 1, a.err, kWaitTimeoutCycles / 16);
-      }
+      if (*abort_flag && issued > 0)  // MMAs already issued finish before TMEM is freed
+        mbar_wait(&s_full[x], (issued - 1) & 1, a.err, kWaitTimeoutCycles / 16);
       __syncwarp();
     }
   } else {
@@ -365,23 +440,26 @@ __global__ void __launch_bounds__(PrefillCfg::THREADS, 1)
       ok = __all_sync(FULL, wait_or_abort(&s_full[x], (t - t0[x]) & 1, abort_flag, a.err));
       if (!ok) break;
       tmem_fence_after();
+      // Loads of 32 scores run beside the maximum of the 32 before.
       uint32_t s[128];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32_async(s_tm + 32 * c, s + 32 * c);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_wait_ld32(s + 32 * c);
       const int j0 = t * C::KT;
-      if (__any_sync(FULL, lo > j0 || hi < j0 + C::KT)) {
+      const bool masked = __any_sync(FULL, lo > j0 || hi < j0 + C::KT);
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      tmem_ld32_async(s_tm, s);
 #pragma unroll
-        for (int k = 0; k < 128; ++k)
-          if (j0 + k < lo || j0 + k >= hi) s[k] = 0xFF800000u;  // -inf
+      for (int c = 0; c < 4; ++c) {
+        tmem_wait_ld32(s + 32 * c);
+        if (c < 3) tmem_ld32_async(s_tm + 32 * (c + 1), s + 32 * (c + 1));
+        if (masked) {
+#pragma unroll
+          for (int k = 32 * c; k < 32 * c + 32; ++k)
+            if (j0 + k < lo || j0 + k >= hi) s[k] = 0xFF800000u;  // -inf
+        }
+#pragma unroll
+        for (int k = 32 * c; k < 32 * c + 32; k += 2)
+          mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
       }
-      float mx[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) mx[k] = __uint_as_float(s[k]);
-#pragma unroll
-      for (int k = 4; k < 128; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(s[k]));
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+      const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * a.scale_log2;
       // The running maximum moves only when a weight would pass 2^8; the warp
       // then moves what its rows have added up so far.
       if (__any_sync(FULL, top - m > 8.f)) {
@@ -400,25 +478,23 @@ __global__ void __launch_bounds__(PrefillCfg::THREADS, 1)
           }
         }
       }
+      // The weights go to the tensor core in halves: it multiplies the first 64
+      // keys' while the second 64 keys' are computed.
       const f32x2 sc2 = f2_pack(a.scale_log2, a.scale_log2), nm2 = f2_pack(-m, -m);
       f32x2 sum2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-      uint32_t p[64];
 #pragma unroll
-      for (int k = 0; k < 128; k += 2) {
-        float u, v;
-        f2_unpack(f2_fma(f2_pack(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), sc2, nm2), u, v);
-        u = fast_exp2(u);
-        v = fast_exp2(v);
-        sum2[(k >> 1) & 1] = f2_add(sum2[(k >> 1) & 1], f2_pack(u, v));
-        p[k >> 1] = pack_bf16x2(u, v);
-        if ((k & 63) == 62) tmem_st32(s_tm + (k >> 6) * 32, p + (k >> 6) * 32);
+      for (int half = 0; half < 2; ++half) {
+        uint32_t p[32];
+        if (masked) weights64<false>(s + 64 * half, sc2, nm2, sum2, p);
+        else weights64<true>(s + 64 * half, sc2, nm2, sum2, p);
+        tmem_st32(s_tm + 32 * half, p);
+        tmem_wait_st();
+        tmem_fence_before();
+        mbar_arrive(&p_full[2 * x + half]);
       }
       float u, v;
       f2_unpack(f2_add(sum2[0], sum2[1]), u, v);
       l += u + v;
-      tmem_wait_st();
-      tmem_fence_before();
-      mbar_arrive(&p_full[x]);
     }
     if (!ok) *abort_flag = 1;
     // ---- normalise and store --------------------------------------------------
@@ -429,7 +505,7 @@ __global__ void __launch_bounds__(PrefillCfg::THREADS, 1)
       tmem_fence_after();
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const long long row = (long long)(qb + i) * a.H + h;
-#pragma unroll 1
+#pragma unroll 2
       for (int c = 0; c < 4; ++c) {
         uint32_t o[32];
         if (any) {
