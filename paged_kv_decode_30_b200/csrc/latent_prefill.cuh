@@ -127,30 +127,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// 2^x of two values in [-inf, 127) on the FMA pipe: x = n + f with n the nearest
-// integer (at least -125), 2^f = 1 + f q(f) on [-1/2, 1/2] with q of degree 4,
-// fitted for the least largest relative error (2^-23.1), 2^n added to the exponent.
-__device__ __forceinline__ void exp2_fma(f32x2 x, float& u, float& v) {
-  float a, b;
-  f2_unpack(x, a, b);
-  x = f2_pack(fmaxf(a, -125.f), fmaxf(b, -125.f));
-  const f32x2 magic = f2_pack(12582912.f, 12582912.f), back = f2_pack(-12582912.f, -12582912.f);
-  const f32x2 t = f2_add(x, magic);  // n in the low bits
-  const f32x2 n = f2_add(t, back);
-  const f32x2 f = f2_fma(n, f2_pack(-1.f, -1.f), x);
-  f32x2 q = f2_pack(0.001326472731307149f, 0.001326472731307149f);
-  q = f2_fma(q, f, f2_pack(0.009671512991189957f, 0.009671512991189957f));
-  q = f2_fma(q, f, f2_pack(0.05550733581185341f, 0.05550733581185341f));
-  q = f2_fma(q, f, f2_pack(0.24022242426872253f, 0.24022242426872253f));
-  q = f2_fma(q, f, f2_pack(0.6931470036506653f, 0.6931470036506653f));
-  q = f2_fma(q, f, f2_pack(1.f, 1.f));
-  float ru, rv, tu, tv;
-  f2_unpack(q, ru, rv);
-  f2_unpack(t, tu, tv);
-  u = __uint_as_float(__float_as_uint(ru) + (__float_as_uint(tu) << 23));
-  v = __uint_as_float(__float_as_uint(rv) + (__float_as_uint(tv) << 23));
-}
-
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -158,24 +134,18 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // Weights 2^(s * scale - m) of 64 scores, as bf16 pairs, and their sum added to
-// `sum`. The special function units alone would take 8 cycles a warp and value;
-// MIX hands one pair in kMixEvery to the FMA pipe. Masked scores (-inf) want
-// exact zeros: no MIX.
-constexpr int kMixEvery = 4;
-template <bool MIX>
+// `sum`. (With a quarter of the exponentials as polynomials on the FMA pipe a
+// step took a tenth fewer cycles, and the long case the same time: at this load
+// the GPU runs at its power limit, 1.55 GHz instead of 1.9.)
 __device__ __forceinline__ void weights64(const uint32_t* s, f32x2 scale2, f32x2 minus_m2, f32x2 (&sum)[2],
                                           uint32_t* p) {
 #pragma unroll
   for (int k = 0; k < 64; k += 2) {
     const f32x2 x = f2_fma(f2_pack(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), scale2, minus_m2);
     float u, v;
-    if (MIX && (k >> 1) % kMixEvery == kMixEvery - 1) {
-      exp2_fma(x, u, v);
-    } else {
-      f2_unpack(x, u, v);
-      u = fast_exp2(u);
-      v = fast_exp2(v);
-    }
+    f2_unpack(x, u, v);
+    u = fast_exp2(u);
+    v = fast_exp2(v);
     sum[(k >> 1) & 1] = f2_add(sum[(k >> 1) & 1], f2_pack(u, v));
     p[k >> 1] = pack_bf16x2(u, v);
   }
@@ -186,9 +156,48 @@ __global__ void __launch_bounds__(PrefillCfg::THREADS, 1)
                           const __grid_constant__ CUtensorMap map_r, const PrefillArgs a) {
   using C = PrefillCfg;
   constexpr unsigned FULL = 0xFFFFFFFFu;
-  // Heads vary fastest, so that the CTAs of one time read few sequences' keys;
-  // the last tiles come first: with a causal mask they see the most keys.
-  const int h = blockIdx.x % a.H, y = blockIdx.x / a.H, b = y % a.B, tile = a.tiles - 1 - y / a.B;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // Heads vary fastest, so that the CTAs of one time read few sequences' keys.
+  // The CTAs start in the order of their index; the longest work comes first,
+  // so that the SMs finish close together. One sequence's tiles are in that
+  // order from the last one down (a causal mask gives it the most keys). Of
+  // several sequences every CTA ranks all (sequence, tile) pairs by their key
+  // tiles, a pair a thread; more pairs than threads keep the order of their tiles.
+  const int h = blockIdx.x % a.H, y = blockIdx.x / a.H, pairs = a.B * a.tiles;
+  int b = y % a.B, tile = a.tiles - 1 - y / a.B;
+  if (a.B > 1 && pairs <= C::THREADS) {
+    int* cost = reinterpret_cast<int*>(smem);
+    int* mine = cost + C::THREADS;
+    const int pb = tid % a.B, pt = a.tiles - 1 - tid / a.B;
+    int c = -1;  // behind the last pair
+    if (tid < pairs) {
+      const int nq = __ldg(a.q_offsets + pb + 1) - __ldg(a.q_offsets + pb);
+      const int nk = __ldg(a.kv_offsets + pb + 1) - __ldg(a.kv_offsets + pb);
+      const int first = pt * 2 * C::QT, last = min(min(nq, a.max_q), first + 2 * C::QT) - 1;
+      c = 0;
+      if (last >= first) {
+        int lo, hi, z;
+        prefill_visible(a, nq, nk, first, lo, z);
+        prefill_visible(a, nq, nk, last, z, hi);
+        c = 1 + max(hi - lo, 0);
+      }
+    }
+    cost[tid] = c;
+    __syncthreads();
+    int rank = 0;
+    for (int k = 0; k < pairs; k += 4) {  // (entries behind the last pair are -1)
+      const int4 o = *reinterpret_cast<const int4*>(cost + k);
+      rank += (o.x > c || (o.x == c && k < tid)) + (o.y > c || (o.y == c && k + 1 < tid)) +
+              (o.z > c || (o.z == c && k + 2 < tid)) + (o.w > c || (o.w == c && k + 3 < tid));
+    }
+    if (tid < pairs && rank == y) *mine = tid;
+    __syncthreads();
+    b = *mine % a.B;
+    tile = a.tiles - 1 - *mine / a.B;
+    __syncthreads();
+  }
   const int qb = __ldg(a.q_offsets + b), nq_all = __ldg(a.q_offsets + b + 1) - qb;
   const int kb = __ldg(a.kv_offsets + b), nk = __ldg(a.kv_offsets + b + 1) - kb;
   if (qb < 0 || nq_all < 0 || nq_all > a.total_q - qb || kb < 0 || nk < 0 || nk > a.total_kv - kb) {
@@ -198,10 +207,7 @@ __global__ void __launch_bounds__(PrefillCfg::THREADS, 1)
   const int row0 = tile * 2 * C::QT, rows = min(min(nq_all, a.max_q) - row0, 2 * C::QT);
   if (rows <= 0) return;
 
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_addr(smem);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // [tile]
   uint64_t* k_full = q_full + 2;   // [stage]
   uint64_t* k_empty = k_full + 2;  // [stage]
@@ -485,8 +491,7 @@ __global__ void __launch_bounds__(PrefillCfg::THREADS, 1)
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         uint32_t p[32];
-        if (masked) weights64<false>(s + 64 * half, sc2, nm2, sum2, p);
-        else weights64<true>(s + 64 * half, sc2, nm2, sum2, p);
+        weights64(s + 64 * half, sc2, nm2, sum2, p);
         tmem_st32(s_tm + 32 * half, p);
         tmem_wait_st();
         tmem_fence_before();
