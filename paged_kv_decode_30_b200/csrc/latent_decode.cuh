@@ -37,6 +37,8 @@
 // Every wait is bounded.
 #pragma once
 
+#include <type_traits>
+
 #include "pda_device.cuh"
 #include "split_tma.cuh"  // MMA issue, instruction descriptors, TMA loads, e4m3 splits
 #include "tcgen05.cuh"
@@ -894,134 +896,158 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
 }
 
 // Joins the partial results of the sequences that lie in several teams' ranges:
-// lse = ln sum_k exp(lse_k), out = sum_k exp(lse_k - lse) o_k. The blocks share
-// the rows of all cut sequences: of a sequence of few parts (most cuts leave
-// two) a warp takes a row, with all its loads in flight at once; of one of many
-// parts a block takes a row, four groups of threads with every fourth part each.
-constexpr int kMergeFew = 4, kMergeTeams = 256;
+// lse = ln sum_k exp(lse_k), out = sum_k exp(lse_k - lse) o_k. Of a sequence of
+// few parts (most cuts leave two or three) a warp takes a row; of one of many
+// parts a block takes a row, WARPS / V warps with every so manyth part each.
+// Bound by latency: the list of cuts, then a row's lse and parts, loaded together.
+constexpr int kMergeFew = 4, kMergeTeams = 256, kMergeThreads = 512;
 
 template <int R>
-__global__ void __launch_bounds__(R, 1024 / R) latent_merge_kernel(const LatentArgs a, int nt) {
+__global__ void __launch_bounds__(kMergeThreads, 2) latent_merge_kernel(const LatentArgs a, int log2_nt) {
   constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
   constexpr unsigned FULL = 0xFFFFFFFFu;
-  constexpr int CT = R / 4, WARPS = R / 32;
-  __shared__ float4 part_o[3][CT];
-  __shared__ int2 cuts[kMergeTeams];        // (team, parts) of the cut sequences
-  __shared__ int ends[kMergeTeams], count;  // work items up to and with each
+  constexpr int WARPS = kMergeThreads / 32, V = R / 128, GROUPS = WARPS / V;
+  __shared__ float4 part_o[GROUPS - 1][V][32];
+  __shared__ int3 cuts[kMergeTeams];  // (team, parts, sequence): those of few parts from the front, the rest from the back
+  __shared__ int2 warp_n[kMergeTeams / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int few_items = (a.M + WARPS - 1) / WARPS;
   pdl_wait_primary();
-  if (warp == 0) {
-    int n = 0, end = 0;
-    for (int t0 = 0; t0 < a.teams; t0 += 32) {
-      const int t = t0 + lane;
-      const int2 c = t < a.teams ? a.cut[t] : make_int2(-1, 0);
-      const int parts = c.x >= 0 ? c.y - t + 1 : 0;
-      int inc = parts == 0 ? 0 : parts <= kMergeFew ? few_items : a.M;
+  int n_few = 0, n_many = 0;
+  {
+    const int2 c = tid < a.teams ? a.cut[tid] : make_int2(-1, 0);
+    const int parts = c.x >= 0 ? c.y - tid + 1 : 0;
+    const bool few = parts > 0 && parts <= kMergeFew, many = parts > kMergeFew;
+    const unsigned f = __ballot_sync(FULL, few), m = __ballot_sync(FULL, many);
+    if (lane == 0 && warp < kMergeTeams / 32) warp_n[warp] = make_int2(__popc(f), __popc(m));
+    __syncthreads();
+    int f0 = 0, m0 = 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(FULL, inc, o);
-        if (lane >= o) inc += y;
+    for (int w = 0; w < kMergeTeams / 32; ++w) {
+      const int2 n = warp_n[w];
+      if (w < warp) {
+        f0 += n.x;
+        m0 += n.y;
       }
-      const unsigned live = __ballot_sync(FULL, parts > 0);
-      if (parts > 0) {
-        const int k = n + __popc(live & ((1u << lane) - 1));
-        cuts[k] = make_int2(t, parts);
-        ends[k] = end + inc;
-      }
-      n += __popc(live);
-      end += __shfl_sync(FULL, inc, 31);
+      n_few += n.x;
+      n_many += n.y;
     }
-    if (lane == 0) count = n;
+    const unsigned below = (1u << lane) - 1;
+    if (few) cuts[f0 + __popc(f & below)] = make_int3(tid, parts, c.x);
+    if (many) cuts[kMergeTeams - 1 - m0 - __popc(m & below)] = make_int3(tid, parts, c.x);
+    __syncthreads();
   }
-  __syncthreads();
-  const int n = count;
-  if (n == 0) return;
-  int c = 0;
-  for (int w = blockIdx.x; w < ends[n - 1]; w += gridDim.x) {
-    while (w >= ends[c]) ++c;
-    const int team = cuts[c].x, parts = cuts[c].y, b = a.cut[team].x;
-    const int in = w - (c > 0 ? ends[c - 1] : 0);
-    const bool few = parts <= kMergeFew;
-    const int row = few ? in * WARPS + warp : in;
-    if (few && row >= a.M) continue;
-    const int rt = row / nt, rr = row - rt * nt;
-    // slot of part k: the piece goes on behind the team's range but in the last
-    auto slot = [&](int k) {
-      return ((long long)((team + k) * a.row_tiles + rt) * 2 + (k + 1 < parts ? 1 : 0)) * nt + rr;
-    };
-    float m = -INFINITY, sum = 0.f;
-    const long long o = (long long)b * a.M + row;
-    if (few) {
-      constexpr int V = R / 128;
-      float l[kMergeFew];
-      const float4* src[kMergeFew];
+  // slot of part k: the piece goes on behind the team's range but in the last
+  auto slot_of = [&](const int3& c, int row, int k) {
+    return ((long long)(((c.x + k) * a.row_tiles + (row >> log2_nt)) * 2 + (k + 1 < c.y ? 1 : 0)) << log2_nt) +
+           (row & ((1 << log2_nt) - 1));
+  };
+  // sum_k exp(lse_k - m) and the largest lse_k, m; l0: this lane's
+  auto row_lse = [&](const int3& c, int row, float l0, float& m) {
+    m = l0;
+    for (int k = lane + 32; k < c.y; k += 32) m = fmaxf(m, a.lse_part[slot_of(c, row, k)]);
 #pragma unroll
-      for (int k = 0; k < kMergeFew; ++k) {
-        const long long s = slot(min(k, parts - 1));
-        l[k] = k < parts ? a.lse_part[s] : -INFINITY;
-        src[k] = reinterpret_cast<const float4*>(a.o_part + s * R) + lane;
-        m = fmaxf(m, l[k]);
-      }
-#pragma unroll
-      for (int k = 0; k < kMergeFew; ++k) sum += l[k] == -INFINITY ? 0.f : exp2f((l[k] - m) * kLog2e);
-      const float lse = m == -INFINITY ? -INFINITY : m + log2f(sum) * kLn2;
-#pragma unroll
-      for (int k = 0; k < kMergeFew; ++k) l[k] = l[k] == -INFINITY ? 0.f : exp2f((l[k] - m) * kLog2e) / sum;
-#pragma unroll 2
-      for (int x = 0; x < V; ++x) {
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f), v[kMergeFew];
-#pragma unroll
-        for (int k = 0; k < kMergeFew; ++k) v[k] = k < parts ? src[k][32 * x] : acc;
-#pragma unroll
-        for (int k = 0; k < kMergeFew; ++k) {
-          acc.x = fmaf(l[k], v[k].x, acc.x);
-          acc.y = fmaf(l[k], v[k].y, acc.y);
-          acc.z = fmaf(l[k], v[k].z, acc.z);
-          acc.w = fmaf(l[k], v[k].w, acc.w);
-        }
-        *reinterpret_cast<uint2*>(a.out + o * R + (lane + 32 * x) * 4) =
-            make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-      }
-      if (lane == 0 && a.lse) a.lse[o] = lse;
-      continue;
+    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
+    float sum = 0.f;
+    if (m != -INFINITY) {
+      sum = exp2f((l0 - m) * kLog2e);
+      for (int k = lane + 32; k < c.y; k += 32) sum += exp2f((a.lse_part[slot_of(c, row, k)] - m) * kLog2e);
     }
-    const int grp = tid / CT, col = tid % CT;
-    for (int k = lane; k < parts; k += 32) m = fmaxf(m, a.lse_part[slot(k)]);
 #pragma unroll
-    for (int x = 16; x >= 1; x >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, x));
-    if (m != -INFINITY)
-      for (int k = lane; k < parts; k += 32) sum += exp2f((a.lse_part[slot(k)] - m) * kLog2e);
+    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+    return sum;
+  };
+  auto store = [&](long long o, int col, const float4& v) {
+    *reinterpret_cast<uint2*>(a.out + o * R + col) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+  };
+
+  // A row of P parts: all its loads go out together (of more than two parts in
+  // two halves of the columns, for the registers).
+  auto few_row = [&](auto parts, const int3& c, int row) {
+    constexpr int P = decltype(parts)::value, X = P <= 2 ? V : V / 2;
+    float l[P], m = -INFINITY;
+    const float4* src[P];
 #pragma unroll
-    for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor_sync(FULL, sum, x);
-    const float lse = m == -INFINITY ? -INFINITY : m + log2f(sum) * kLn2;
+    for (int k = 0; k < P; ++k) {
+      const long long s = slot_of(c, row, k);
+      l[k] = a.lse_part[s];
+      src[k] = reinterpret_cast<const float4*>(a.o_part + s * R) + lane;
+    }
+    const long long o = (long long)c.z * a.M + row;
+#pragma unroll
+    for (int x0 = 0; x0 < V; x0 += X) {
+      float4 q[X][P];
+#pragma unroll
+      for (int x = 0; x < X; ++x)
+#pragma unroll
+        for (int k = 0; k < P; ++k) q[x][k] = src[k][32 * (x0 + x)];
+      if (x0 == 0) {  // the parts' weights, and the row's lse
+#pragma unroll
+        for (int k = 0; k < P; ++k) m = fmaxf(m, l[k]);
+        const float base = m == -INFINITY ? 0.f : m;
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < P; ++k) sum += l[k] = fast_exp2((l[k] - base) * kLog2e);
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+        for (int k = 0; k < P; ++k) l[k] *= inv;
+        if (lane == 0 && a.lse) a.lse[o] = m == -INFINITY ? -INFINITY : m + log2f(sum) * kLn2;
+      }
+#pragma unroll
+      for (int x = 0; x < X; ++x) {
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+          acc.x = fmaf(l[k], q[x][k].x, acc.x);
+          acc.y = fmaf(l[k], q[x][k].y, acc.y);
+          acc.z = fmaf(l[k], q[x][k].z, acc.z);
+          acc.w = fmaf(l[k], q[x][k].w, acc.w);
+        }
+        store(o, (lane + 32 * (x0 + x)) * 4, acc);
+      }
+    }
+  };
+  for (int u = blockIdx.x * WARPS + warp; u < n_few * a.M; u += gridDim.x * WARPS) {
+    const int ci = u / a.M, row = u - ci * a.M;
+    const int3 c = cuts[ci];
+    if (c.y == 2) few_row(std::integral_constant<int, 2>{}, c, row);
+    else if (c.y == 3) few_row(std::integral_constant<int, 3>{}, c, row);
+    else few_row(std::integral_constant<int, 4>{}, c, row);
+  }
+
+  for (int u = blockIdx.x; u < n_many * a.M; u += gridDim.x) {
+    const int ci = u / a.M, row = u - ci * a.M;
+    const int3 c = cuts[kMergeTeams - 1 - ci];
+    const int x = warp % V, grp = warp / V;
+    const float l0 = lane < c.y ? a.lse_part[slot_of(c, row, lane)] : -INFINITY;
+    float m;
+    const float sum = row_lse(c, row, l0, m);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (m != -INFINITY) {
-#pragma unroll 4
-      for (int k = grp; k < parts; k += 4) {
-        const long long s = slot(k);
-        const float wgt = exp2f((a.lse_part[s] - m) * kLog2e) / sum;  // 0 for a part without keys
-        const float4 v = *reinterpret_cast<const float4*>(a.o_part + s * R + col * 4);
-        acc.x = fmaf(wgt, v.x, acc.x);
-        acc.y = fmaf(wgt, v.y, acc.y);
-        acc.z = fmaf(wgt, v.z, acc.z);
-        acc.w = fmaf(wgt, v.w, acc.w);
+#pragma unroll 8
+      for (int k = grp; k < c.y; k += GROUPS) {
+        const long long s = slot_of(c, row, k);
+        const float w = exp2f((a.lse_part[s] - m) * kLog2e) / sum;  // 0 for a part without keys
+        const float4 q = *(reinterpret_cast<const float4*>(a.o_part + s * R) + lane + 32 * x);
+        acc.x = fmaf(w, q.x, acc.x);
+        acc.y = fmaf(w, q.y, acc.y);
+        acc.z = fmaf(w, q.z, acc.z);
+        acc.w = fmaf(w, q.w, acc.w);
       }
     }
-    if (grp > 0) part_o[grp - 1][col] = acc;
+    if (grp > 0) part_o[grp - 1][x][lane] = acc;
     __syncthreads();
     if (grp == 0) {
 #pragma unroll
-      for (int x = 0; x < 3; ++x) {
-        const float4 v = part_o[x][col];
-        acc.x += v.x;
-        acc.y += v.y;
-        acc.z += v.z;
-        acc.w += v.w;
+      for (int k = 0; k < GROUPS - 1; ++k) {
+        const float4 q = part_o[k][x][lane];
+        acc.x += q.x;
+        acc.y += q.y;
+        acc.z += q.z;
+        acc.w += q.w;
       }
-      *reinterpret_cast<uint2*>(a.out + o * R + col * 4) =
-          make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-      if (col == 0 && a.lse) a.lse[o] = lse;
+      const long long o = (long long)c.z * a.M + row;
+      store(o, (lane + 32 * x) * 4, acc);
+      if (x == 0 && lane == 0 && a.lse) a.lse[o] = m == -INFINITY ? -INFINITY : m + log2f(sum) * kLn2;
     }
     __syncthreads();
   }

@@ -1,6 +1,8 @@
 // Launch of one latent decode variant: tensor maps, the kernel, the merge.
 #pragma once
 
+#include <algorithm>
+
 #include "latent_decode.cuh"
 #include "latent_decode.h"
 #include "tensor_map.cuh"
@@ -58,15 +60,15 @@ cudaError_t launch_latent(const LatentCall& c, cudaStream_t stream) {
   e = cudaGetLastError();
   if (e != cudaSuccess || a.teams == 1) return e;  // one team cuts no sequence
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.teams * a.row_tiles * (1024 / R)));
-  cfg.blockDim = dim3(R);
+  cfg.gridDim = dim3((unsigned)std::min(a.teams * a.row_tiles * 2, 2 * kMergeTeams));
+  cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = (p.flags & PDA_FLAG_NO_PDL) ? 0 : 1;
-  return cudaLaunchKernelEx(&cfg, latent_merge_kernel<R>, a, NT);
+  return cudaLaunchKernelEx(&cfg, latent_merge_kernel<R>, a, NT == 16 ? 4 : NT == 32 ? 5 : 6);
 }
 
 }  // namespace pda
