@@ -110,7 +110,16 @@ struct LatentCfg {
   static constexpr int R = R_, NT = NT_, NB = R / 128;
   static constexpr bool FP8 = FP8_;
   static constexpr int HALF = kTile * 128;              // a 128-byte column of a tile
-  static constexpr int BLK = FP8 ? HALF : 2 * HALF;     // 128 elements of a tile's rows
+  // A tile lies in shared memory as [8-token group][128-byte column][8 tokens]
+  // [128 bytes], the order in which one TMA box writes a run of tokens. It comes
+  // in units with barriers of their own: bf16 128 elements of 128 tokens (a tile
+  // and little more fit, so S^T starts on what is there), FP8 whole rows of 64
+  // tokens (two tiles fit; fewer, larger copies).
+  static constexpr int COLS_U = FP8 ? NB : 2;           // 128-byte columns of a unit
+  static constexpr int GS = COLS_U * 1024;              // bytes of an 8-token group
+  static constexpr int UT = FP8 ? 64 : 128;             // tokens of a unit
+  static constexpr int UPT = FP8 ? 2 : NB;              // units of a tile
+  static constexpr int BLK = UT / 8 * GS;
   static constexpr int N1 = FP8 ? 2 * NT : NT;          // S^T columns of the latent product
   static constexpr int N2 = FP8 ? 2 * NT : NT;          // O^T columns of a block
   static constexpr int SN = FP8 ? 3 * NT : NT;          // S^T columns (FP8: rotated part apart)
@@ -122,8 +131,8 @@ struct LatentCfg {
   static constexpr int P_ROW = 2 * NT;                  // bytes of a token's weights
   static constexpr int P_BYTES = kTile * P_ROW;
   static constexpr uint32_t P_SWIZZLE = P_ROW == 128 ? kSw128 : P_ROW == 64 ? kSw64 : kSw32;
-  // Shared memory is Q, weights, the rotated parts' slot and as many 128-element
-  // blocks of latents as fit. The widest bf16 case has room for one tile only
+  // Shared memory is Q, weights, the rotated parts' slots and as many units of
+  // latents as fit. The widest bf16 case has room for one tile only
   // if the weights take the place of the rotated parts, which the S^T product
   // has read by then.
   static constexpr bool OVERLAY = !FP8 && NT == 64 && R == 512;
@@ -133,7 +142,8 @@ struct LatentCfg {
   static constexpr int STATE = 20 * NT * 4 + 1024;
   static constexpr int FREE = 227 * 1024 - 1024 - STATE - Q_BYTES - (OVERLAY ? 0 : P_BUFS * P_BYTES) -
                               R_SLOTS * ROPE_SLOT;
-  static constexpr int SLOTS = FREE / BLK < 3 * NB ? FREE / BLK : 3 * NB;
+  static constexpr int FIT = FREE / BLK < 3 * UPT ? FREE / BLK : 3 * UPT;
+  static constexpr int SLOTS = FP8 ? FIT / 2 * 2 : FIT;  // FP8 tiles do not wrap around
   static constexpr int OFF_BLK = 0;
   static constexpr int OFF_ROPE = OFF_BLK + SLOTS * BLK;
   static constexpr int OFF_Q = OFF_ROPE + R_SLOTS * ROPE_SLOT;
@@ -162,12 +172,23 @@ struct LatentCfg {
   static constexpr int COL_O = 0, COL_S = NB * N2;
   static constexpr int COLS = COL_S + 2 * SN;
   static constexpr int TMEM_COLS = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
-  static_assert(COLS <= 512 && SLOTS >= NB && SMEM_ALLOC <= 227 * 1024, "capacity");
+  static_assert(COLS <= 512 && SLOTS >= UPT && SMEM_ALLOC <= 227 * 1024, "capacity");
   static_assert(BLK % 1024 == 0 && Q_BLK % 1024 == 0 && Q_BYTES % 1024 == 0 && P_BYTES % 1024 == 0, "alignment");
   // Weights are at most 2^8 (e4m3 holds 448). FP8 starts them at 2^4, which
   // keeps the second term's smallest step 2^18 below the largest weight.
   static constexpr float HEAD = FP8 ? 4.f : 0.f;
 };
+
+// Loads `box` tokens from token group `group` on, of every token the 128-byte
+// columns from `col` on (make_tokens_map).
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int col, int group,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(0), "r"(col), "r"(group), "r"(smem_addr(bar))
+      : "memory");
+}
 
 // 128-byte-swizzled address of 16-byte piece c of row n in a block of rows.
 __device__ __forceinline__ uint32_t sw128(int n, int c) {
@@ -218,7 +239,7 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
   const int team = blockIdx.x / a.row_tiles, rt = blockIdx.x % a.row_tiles;
 
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // [SLOTS] latents landed
-  uint64_t* empty = full + C::SLOTS;         // [SLOTS] O^T of the block done
+  uint64_t* empty = full + C::SLOTS;         // [SLOTS] its O^T products done
   uint64_t* rfull = empty + C::SLOTS;        // [R_SLOTS] rotated parts landed
   uint64_t* rempty = rfull + C::R_SLOTS;     // [R_SLOTS] and read (overlay: and the weights too)
   uint64_t* s_full = rempty + C::R_SLOTS;    // [2] S^T in TMEM
@@ -369,13 +390,13 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
     __syncwarp();
   } else if (warp == 0) {
     // ======================= TMA producer (whole warp) =========================
-    // Lane g copies page segment g of a tile. Block k of tile t (counted over
-    // all items) goes to slot (t * NB + k) % SLOTS.
+    // Unit u of tile t (counted over all items) goes to slot (t * UPT + u) % SLOTS.
+    // Lane g copies page segment g of the unit's tokens.
     if (lane == 0) {
       asm volatile("prefetch.tensormap [%0];" ::"l"(&map_c) : "memory");
       asm volatile("prefetch.tensormap [%0];" ::"l"(&map_r) : "memory");
     }
-    const int seg_rows = min(a.page_size, kTile);
+    const int seg_rows = min(a.page_size, C::UT), log2_seg = min(a.log2_page, FP8 ? 6 : 7);
     int g = 0, blk = 0;
     bool ok = true;
     for (int j = 0; ok; ++j) {
@@ -386,13 +407,11 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
       if (lane == 0) mbar_arrive(&item_free[j % C::ITEMS]);
       if (d.b < 0) break;
       const int32_t* pt = a.page_table + (long long)d.b * a.max_pages;
-      const int pages = (d.L + a.page_size - 1) >> a.log2_page;
-      auto segments = [&](int t) {
-        return a.page_size >= kTile ? 1 : min(kTile >> a.log2_page, pages - ((t * kTile) >> a.log2_page));
-      };
-      auto page_of = [&](int t) -> int {  // this lane's page of tile t
+      // segments of tile t that hold tokens, counted from the tile's first token
+      auto segments = [&](int t) { return min(kTile, d.L - t * kTile + seg_rows - 1) >> log2_seg; };
+      auto page_of = [&](int t) -> int {  // the page of this lane's segment of tile t
         if (t >= d.first + d.n || lane >= segments(t)) return 0;
-        return __ldg(pt + ((t * kTile) >> a.log2_page) + lane);
+        return __ldg(pt + ((t * kTile + lane * seg_rows) >> a.log2_page));
       };
       int pid = page_of(d.first), pid_next = page_of(d.first + 1);
       for (int t = d.first; ok && t < d.first + d.n; ++t, ++g) {
@@ -401,25 +420,24 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
           record_error_at(a.err, kErrBadPage);
           pid = 0;
         }
-        const int row = pid * a.page_size + (a.page_size >= kTile ? (t * kTile) & (a.page_size - 1) : 0);
-        const uint32_t off = (uint32_t)lane * seg_rows * 128u;
-        const uint32_t bytes = (uint32_t)(nseg * seg_rows) * 128u;
+        const int row = pid * a.page_size + ((t * kTile + lane * seg_rows) & (a.page_size - 1));
         pid = pid_next;
         pid_next = page_of(t + 2);
 #pragma unroll 1
-        for (int k = 0; k < C::NB; ++k, ++blk) {
+        for (int k = 0; k < C::UPT; ++k, ++blk) {
           const int sl = blk % C::SLOTS;
           if (blk >= C::SLOTS) {
             ok = __all_sync(FULL, wait_or_abort(&empty[sl], ((blk / C::SLOTS) - 1) & 1, abort_flag, a.err));
             if (!ok) break;
           }
-          if (lane == 0) mbar_arrive_expect_tx(&full[sl], FP8 ? bytes : 2 * bytes);
+          // FP8: this unit's segments are lanes [s0, s0 + per)
+          const int per = C::UT >> log2_seg, s0 = FP8 ? k * per : 0;
+          const int cnt = FP8 ? min(max(nseg - s0, 0), per) : nseg;
+          if (lane == 0) mbar_arrive_expect_tx(&full[sl], (uint32_t)((cnt * seg_rows) >> 3) * C::GS);
           __syncwarp();
-          if (lane < nseg) {
-            const uint32_t dst = sbase + C::OFF_BLK + sl * C::BLK + off;
-            tma_load_2d(dst, &map_c, k * 128, row, &full[sl]);
-            if constexpr (!FP8) tma_load_2d(dst + C::HALF, &map_c, k * 128 + 64, row, &full[sl]);
-          }
+          if (lane >= s0 && lane < s0 + cnt)
+            tma_load_4d(sbase + C::OFF_BLK + sl * C::BLK + (((lane - s0) * seg_rows) >> 3) * C::GS, &map_c,
+                        FP8 ? 0 : 2 * k, row >> 3, &full[sl]);
         }
         if (!ok) break;
         const int rs = g % C::R_SLOTS;
@@ -427,9 +445,10 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
           ok = __all_sync(FULL, wait_or_abort(&rempty[rs], ((g / C::R_SLOTS) - 1) & 1, abort_flag, a.err));
           if (!ok) break;
         }
-        if (lane == 0) mbar_arrive_expect_tx(&rfull[rs], bytes);
+        if (lane == 0) mbar_arrive_expect_tx(&rfull[rs], (uint32_t)(nseg * seg_rows) * 128u);
         __syncwarp();
-        if (lane < nseg) tma_load_2d(sbase + C::OFF_ROPE + rs * C::ROPE_SLOT + off, &map_r, 0, row, &rfull[rs]);
+        if (lane < nseg)
+          tma_load_2d(sbase + C::OFF_ROPE + rs * C::ROPE_SLOT + lane * seg_rows * 128, &map_r, 0, row, &rfull[rs]);
       }
     }
     if (!ok) {
@@ -468,28 +487,41 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
           if (g >= 2) ok = agreed(wait_or_abort(&p_ready[bb], ((g - 2) >> 1) & 1, abort_flag, a.err));
           const uint32_t dt = tmem + C::COL_S + bb * C::SN;
           const uint64_t q0 = umma_desc(sbase + C::OFF_Q, 16, 1024, kSw128);
-#pragma unroll 1
-          for (int k = 0; ok && k < C::NB; ++k, ++blk) {
+          if constexpr (FP8) {
             const int sl = blk % C::SLOTS;
-            ok = agreed(wait_or_abort(&full[sl], (blk / C::SLOTS) & 1, abort_flag, a.err));
+            ok = ok && agreed(wait_or_abort(&full[sl], (blk / C::SLOTS) & 1, abort_flag, a.err) &&
+                              wait_or_abort(&full[sl + 1], (blk / C::SLOTS) & 1, abort_flag, a.err));
             if (!ok) break;
             tmem_fence_after();
-            const uint64_t ca = umma_desc(sbase + C::OFF_BLK + sl * C::BLK, 16, 1024, kSw128);
-            const uint64_t qb = q0 + ((k * C::Q_BLK) >> 4);
             if (leader) {
-              if constexpr (FP8) {
-                constexpr uint32_t idesc = umma_idesc_e4m3(128, C::N1);
+              constexpr uint32_t idesc = umma_idesc_e4m3(128, C::N1);
+              const uint64_t ca = umma_desc(sbase + C::OFF_BLK + sl * C::BLK, 16, C::GS, kSw128);
 #pragma unroll
-                for (int s = 0; s < 4; ++s) umma_f8(dt, ca + 2 * s, qb + 2 * s, idesc, k > 0 || s > 0);
-              } else {
+              for (int k = 0; k < C::NB; ++k)
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                  umma_f8(dt, ca + ((k * 1024 + s * 32) >> 4), q0 + ((k * C::Q_BLK + s * 32) >> 4), idesc, k > 0 || s > 0);
+            }
+            __syncwarp();
+            blk += C::UPT;
+          } else {
+#pragma unroll 1
+            for (int k = 0; ok && k < C::NB; ++k, ++blk) {
+              const int sl = blk % C::SLOTS;
+              ok = agreed(wait_or_abort(&full[sl], (blk / C::SLOTS) & 1, abort_flag, a.err));
+              if (!ok) break;
+              tmem_fence_after();
+              const uint64_t ca = umma_desc(sbase + C::OFF_BLK + sl * C::BLK, 16, C::GS, kSw128);
+              const uint64_t qb = q0 + ((k * C::Q_BLK) >> 4);
+              if (leader) {
                 constexpr uint32_t idesc = umma_idesc_bf16(128, NT, false, false);
 #pragma unroll
                 for (int s = 0; s < 8; ++s)
-                  umma_f16(dt, ca + (((s >> 2) * C::HALF + (s & 3) * 32) >> 4),
+                  umma_f16(dt, ca + (((s >> 2) * 1024 + (s & 3) * 32) >> 4),
                            qb + (((s >> 2) * (NT * 128) + (s & 3) * 32) >> 4), idesc, k > 0 || s > 0);
               }
+              __syncwarp();
             }
-            __syncwarp();
           }
           const int rs = g % C::R_SLOTS;
           ok = agreed(ok && wait_or_abort(&rfull[rs], (g / C::R_SLOTS) & 1, abort_flag, a.err));
@@ -518,26 +550,37 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
           tmem_fence_after();
           constexpr uint32_t SBO = 8 * C::P_ROW;
           const uint64_t pd = umma_desc(sbase + C::OFF_P + (g % C::P_BUFS) * C::P_BYTES, C::P_BYTES, SBO, C::P_SWIZZLE);
-#pragma unroll 1
-          for (int k = 0; k < C::NB; ++k, ++blk) {
+          if constexpr (FP8) {  // 32 tokens at a time, all blocks
             const int sl = blk % C::SLOTS;
-            const uint64_t ca = umma_desc(sbase + C::OFF_BLK + sl * C::BLK, C::HALF, 1024, kSw128);
-            const uint32_t dt = tmem + C::COL_O + k * C::N2;
+            const uint64_t ca = umma_desc(sbase + C::OFF_BLK + sl * C::BLK, 1024, C::GS, kSw128);
             if (leader) {
-              if constexpr (FP8) {
-                constexpr uint32_t idesc = umma_idesc_e4m3_mn(128, C::N2);
+              constexpr uint32_t idesc = umma_idesc_e4m3_mn(128, C::N2);
 #pragma unroll
-                for (int s = 0; s < 4; ++s)
-                  umma_f8(dt, ca + ((s * 4096) >> 4), pd + ((s * 4 * SBO) >> 4), idesc, t > 0 || s > 0);
-              } else {
+              for (int s = 0; s < 4; ++s) {
+#pragma unroll
+                for (int k = 0; k < C::NB; ++k)
+                  umma_f8(tmem + C::COL_O + k * C::N2, ca + ((s * 4 * C::GS + k * 1024) >> 4),
+                          pd + ((s * 4 * SBO) >> 4), idesc, t > 0 || s > 0);
+                if (s & 1) umma_commit(&empty[sl + (s >> 1)]);
+              }
+            }
+            __syncwarp();
+            blk += C::UPT;
+          } else {
+#pragma unroll 1
+            for (int k = 0; k < C::NB; ++k, ++blk) {
+              const int sl = blk % C::SLOTS;
+              const uint64_t ca = umma_desc(sbase + C::OFF_BLK + sl * C::BLK, 1024, C::GS, kSw128);
+              const uint32_t dt = tmem + C::COL_O + k * C::N2;
+              if (leader) {
                 constexpr uint32_t idesc = umma_idesc_bf16(128, C::N2, true, true);
 #pragma unroll
                 for (int s = 0; s < 8; ++s)
-                  umma_f16(dt, ca + ((s * 2048) >> 4), pd + ((s * 2 * SBO) >> 4), idesc, t > 0 || s > 0);
+                  umma_f16(dt, ca + ((s * 2 * C::GS) >> 4), pd + ((s * 2 * SBO) >> 4), idesc, t > 0 || s > 0);
+                umma_commit(&empty[sl]);
               }
-              umma_commit(&empty[sl]);
+              __syncwarp();
             }
-            __syncwarp();
           }
           if (leader) {
             if constexpr (C::OVERLAY) umma_commit(&rempty[g % C::R_SLOTS]);
@@ -700,12 +743,14 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
           // before they meet its zero weights. The groups share the blocks.
           if (good && (jt < d.lo_u || jt >= d.hi_u)) {
             for (int k = grp; k < C::NB; k += C::GROUPS) {
-              uint8_t* row = smem + C::OFF_BLK + ((g * C::NB + k) % C::SLOTS) * C::BLK + i * 128;
+              const int u = g * C::UPT + (FP8 ? 0 : k);
+              uint8_t* row = smem + C::OFF_BLK + (u % C::SLOTS) * C::BLK + (i >> 3) * C::GS + (i & 7) * 128 +
+                             (FP8 ? k * 1024 : 0);
 #pragma unroll
               for (int c = 0; c < 8; ++c) {
                 const int cc = (c + i) & 7;
                 *reinterpret_cast<uint4*>(row + cc * 16) = make_uint4(0, 0, 0, 0);
-                if constexpr (!FP8) *reinterpret_cast<uint4*>(row + C::HALF + cc * 16) = make_uint4(0, 0, 0, 0);
+                if constexpr (!FP8) *reinterpret_cast<uint4*>(row + 1024 + cc * 16) = make_uint4(0, 0, 0, 0);
               }
             }
           }
@@ -849,9 +894,10 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
         float o[RH];
 #pragma unroll
         for (int r = 0; r < RH; ++r) o[r] = 0.f;
-        if (n > 0) {  // block k of the last tile has been added
+        if (n > 0) {  // the last tile's products (bf16: of block k) are done
           const int blk = (g - 1) * C::NB + k;
-          good = good && wait_or_abort(&empty[blk % C::SLOTS], (blk / C::SLOTS) & 1, abort_flag, a.err);
+          good = good && (FP8 ? wait_or_abort(&o_full[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag, a.err)
+                              : wait_or_abort(&empty[blk % C::SLOTS], (blk / C::SLOTS) & 1, abort_flag, a.err));
           if (!__all_sync(FULL, good)) break;
           tmem_fence_after();
           if constexpr (FP8) {

@@ -39,9 +39,9 @@ cudaError_t launch_latent(const LatentCall& c, cudaStream_t stream) {
   a.row_tiles = c.row_tiles;
   a.scale_log2 = p.scale * 1.4426950408889634f;
   const long long rows = (long long)p.num_pages * p.page_size;
-  const int box = p.page_size < kTile ? p.page_size : kTile;
+  const int box = p.page_size < C::UT ? p.page_size : C::UT;
   alignas(64) CUtensorMap mc, mr, mq;
-  if (!make_rows_map(&mc, c.latent_pages, R, rows, R, FP8 ? 1 : 2, box) ||
+  if (!make_tokens_map(&mc, c.latent_pages, R, rows, FP8 ? 1 : 2, box, C::COLS_U) ||
       !make_rows_map(&mr, c.rope_pages, p.rope_dim, rows, p.rope_dim, 2, box) ||
       !make_rows_map(&mq, c.q, R + p.rope_dim, (long long)a.B * a.M, R + p.rope_dim, 2, NT))
     return cudaErrorInvalidValue;

@@ -63,4 +63,23 @@ inline bool make_heads_map(CUtensorMap* map, const void* base, long long width, 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Rows of `width` elements (elt bytes: 1 or 2 = bf16), contiguous, as [groups of
+// 8 rows][128-byte columns][8 rows][128 bytes]: boxes of box_rows rows (a
+// multiple of 8, as is `rows`) x box_cols columns arrive in that order, each 8 x
+// 128 bytes swizzled.
+inline bool make_tokens_map(CUtensorMap* map, const void* base, long long width, long long rows, int elt,
+                            int box_rows, int box_cols) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t row = (cuuint64_t)(width * elt);
+  const cuuint64_t dims[4] = {(cuuint64_t)(128 / elt), 8, row / 128, (cuuint64_t)(rows / 8)};
+  const cuuint64_t strides[3] = {row, 128, 8 * row};
+  const cuuint32_t box[4] = {(cuuint32_t)(128 / elt), 8, (cuuint32_t)box_cols, (cuuint32_t)(box_rows / 8)};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, elt == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace pda
