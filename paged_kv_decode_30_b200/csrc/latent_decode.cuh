@@ -149,7 +149,7 @@ struct LatentCfg {
   static constexpr int OFF_Q = OFF_ROPE + R_SLOTS * ROPE_SLOT;
   static constexpr int OFF_P = OVERLAY ? OFF_ROPE : OFF_Q + Q_BYTES;
   static constexpr int OFF_STATE = OVERLAY ? OFF_Q + Q_BYTES : OFF_P + P_BUFS * P_BYTES;
-  static constexpr int OFF_M = OFF_STATE;               // running maximum per row
+  static constexpr int OFF_M = OFF_STATE;               // running maximum per row, negated
   static constexpr int OFF_ALPHA = OFF_M + NT * 4;
   static constexpr int OFF_WMAX = OFF_ALPHA + NT * 4;   // [4][NT]
   static constexpr int OFF_LRED = OFF_WMAX + 4 * NT * 4;   // [2][4][NT]: sums of weights, of rounded ones
@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
     const int q4 = warp & 3, grp = (warp - C::SOFT) >> 2, gbar = 2 + grp, r0 = RH * grp;
     const int i = 32 * q4 + lane;
     const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
-    float* sm_m = reinterpret_cast<float*>(smem + C::OFF_M);
+    float* sm_nm = reinterpret_cast<float*>(smem + C::OFF_M);
     float* sm_alpha = reinterpret_cast<float*>(smem + C::OFF_ALPHA);
     float* wmax = reinterpret_cast<float*>(smem + C::OFF_WMAX);
     float* lred = reinterpret_cast<float*>(smem + C::OFF_LRED);
@@ -690,7 +690,7 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
         int lo = 0, hi = 0;
         if (R0 + i < a.M) latent_visible(a, L, (R0 + i) / a.H, lo, hi);
         sm_range[r0 + i] = make_int2(lo, hi);
-        sm_m[r0 + i] = kUnset;
+        sm_nm[r0 + i] = -kUnset;
       }
       named_bar(gbar, GT);
       // FP8: this token's scale exponent, looked up a tile ahead
@@ -711,34 +711,32 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
         const float e_tok = FP8 ? (float)(min(max(sc_next, 97), 157) - 127) : 0.f;
         sc_next = scale_of(t + 1);
         bool good = __all_sync(FULL, wait_or_abort(&s_full[bb], (g >> 1) & 1, abort_flag, a.err));
-        float x[RH];
+        // Raw scores; FP8: hi + lo / 16 of the latent parts, and the rotated parts.
+        float sc[RH], se[FP8 ? RH : 1];
         if (good) {
           tmem_fence_after();
           const uint32_t ta = s_tm + bb * C::SN;
           if constexpr (FP8) {
-            const float up = __int_as_float((int)(e_tok + 127.f) << 23);
-            float hl[2 * RH], y[RH];
+            float hl[2 * RH];
             tmem_ldn(ta, hl);
-            tmem_ldn(tmem + lane_off + C::COL_S + bb * C::SN + C::N1 + r0, y);
+            tmem_ldn(tmem + lane_off + C::COL_S + bb * C::SN + C::N1 + r0, se);
 #pragma unroll
-            for (int r = 0; r < RH; ++r)
-              x[r] = fmaf(y[r], a.scale_log2, fmaf(hl[RH + r], 0.0625f, hl[r]) * up * sm_cs[r0 + r]) + e_tok;
+            for (int r = 0; r < RH; r += 2)
+              f2_unpack(f2_fma(f2_pack(hl[RH + r], hl[RH + r + 1]), f2_pack(0.0625f, 0.0625f), f2_pack(hl[r], hl[r + 1])),
+                        sc[r], sc[r + 1]);
           } else {
-            tmem_ldn(ta, x);
-#pragma unroll
-            for (int r = 0; r < RH; ++r) x[r] *= a.scale_log2;
+            tmem_ldn(ta, sc);
           }
         } else {
 #pragma unroll
-          for (int r = 0; r < RH; ++r) x[r] = -INFINITY;
+          for (int r = 0; r < RH; ++r) sc[r] = -INFINITY;
+          if constexpr (FP8)
+#pragma unroll
+            for (int r = 0; r < RH; ++r) se[r] = 0.f;
         }
         const int t0 = t * kTile, jt = t0 + i;
-        if (!(t0 >= d.lo_x && t0 + kTile <= d.hi_x)) {
-#pragma unroll
-          for (int r = 0; r < RH; ++r) {
-            const int2 v = sm_range[r0 + r];
-            if (!(jt >= v.x && jt < v.y)) x[r] = -INFINITY;
-          }
+        const bool clean = t0 >= d.lo_x && t0 + kTile <= d.hi_x;
+        if (!clean) {
           // A token that no row sees may hold NaN: its latents become zeros
           // before they meet its zero weights. The groups share the blocks.
           if (good && (jt < d.lo_u || jt >= d.hi_u)) {
@@ -755,19 +753,46 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
             }
           }
         }
+        // Scores in log2 units less the rows' running maxima (or as they are),
+        // FP8 with the token's exponent added; -inf where the row does not see
+        // the token. Two rows an instruction.
+        const f32x2 scale2 = f2_pack(a.scale_log2, a.scale_log2);
+        auto relative = [&](bool less_max, float (&x)[RH]) {
+#pragma unroll
+          for (int r = 0; r < RH; r += 2) {
+            const f32x2 base = less_max ? *reinterpret_cast<const f32x2*>(sm_nm + r0 + r) : f2_pack(0.f, 0.f);
+            f32x2 v;
+            if constexpr (FP8) {
+              const float up = __int_as_float((int)(e_tok + 127.f) << 23);
+              v = f2_fma(f2_pack(se[r], se[r + 1]), scale2, f2_add(base, f2_pack(e_tok, e_tok)));
+              v = f2_fma(f2_pack(sc[r], sc[r + 1]),
+                         f2_mul(*reinterpret_cast<const f32x2*>(sm_cs + r0 + r), f2_pack(up, up)), v);
+            } else {
+              v = f2_fma(f2_pack(sc[r], sc[r + 1]), scale2, base);
+            }
+            f2_unpack(v, x[r], x[r + 1]);
+          }
+          if (!clean) {
+#pragma unroll
+            for (int r = 0; r < RH; ++r) {
+              const int2 v = sm_range[r0 + r];
+              if (!(jt >= v.x && jt < v.y)) x[r] = -INFINITY;
+            }
+          }
+        };
+        float x[RH];
+        relative(true, x);
         // The running maximum moves only when a score passes it by so much that
         // a weight would pass 2^8; most tiles skip the exchange.
-        bool want = !good;
+        float top = x[0];
 #pragma unroll
-        for (int r = 0; r < RH; r += 4) {
-          const float4 m = reinterpret_cast<const float4*>(sm_m + r0)[r / 4];
-          want |= (x[r] - m.x > 8.f) | (x[r + 1] - m.y > 8.f) | (x[r + 2] - m.z > 8.f) | (x[r + 3] - m.w > 8.f);
-        }
-        if (named_bar_or(gbar, GT, want)) {
+        for (int r = 1; r < RH; ++r) top = fmaxf(top, x[r]);
+        if (named_bar_or(gbar, GT, !good || top > 8.f)) {
           if (!named_bar_and(gbar, GT, good)) {
             ok = false;
             break;
           }
+          relative(false, x);
 #pragma unroll
           for (int r = 0; r < RH; ++r) {
             const float wm = redux_max(x[r]);
@@ -776,10 +801,10 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
           named_bar(gbar, GT);
           if (i < RH) {
             const int rr = r0 + i;
-            const float top = fmaxf(fmaxf(wmax[rr], wmax[NT + rr]), fmaxf(wmax[2 * NT + rr], wmax[3 * NT + rr]));
-            const float m_old = sm_m[rr], m_new = fmaxf(m_old, top - C::HEAD);
+            const float most = fmaxf(fmaxf(wmax[rr], wmax[NT + rr]), fmaxf(wmax[2 * NT + rr], wmax[3 * NT + rr]));
+            const float m_old = -sm_nm[rr], m_new = fmaxf(m_old, most - C::HEAD);
             sm_alpha[rr] = fast_exp2(m_old - m_new);
-            sm_m[rr] = m_new;
+            sm_nm[rr] = -m_new;
           }
           named_bar(gbar, GT);
           float al[RH];
@@ -807,15 +832,10 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
               *abort_flag = 1;
             }
           }
+          relative(true, x);
         }
 #pragma unroll
-        for (int r = 0; r < RH; r += 4) {
-          const float4 m = reinterpret_cast<const float4*>(sm_m + r0)[r / 4];
-          x[r] = fast_exp2(x[r] - m.x);
-          x[r + 1] = fast_exp2(x[r + 1] - m.y);
-          x[r + 2] = fast_exp2(x[r + 2] - m.z);
-          x[r + 3] = fast_exp2(x[r + 3] - m.w);
-        }
+        for (int r = 0; r < RH; ++r) x[r] = fast_exp2(x[r]);
         uint32_t w[RH / 2];  // FP8: first terms, then second terms; bf16: pairs
         if constexpr (FP8) {
 #pragma unroll
@@ -844,18 +864,13 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
         tmem_fence_before();
         mbar_arrive(&p_ready[bb]);
         // the sums, beside the products
-        if constexpr (FP8) {
-          const float down = __int_as_float((int)(127.f - e_tok) << 23);
+        const float down = FP8 ? __int_as_float((int)(127.f - e_tok) << 23) : 1.f;
 #pragma unroll
-          for (int r = 0; r < RH; ++r) l_sum[r] = fmaf(x[r], down, l_sum[r]);
-        } else {
-#pragma unroll
-          for (int r = 0; r < RH; r += 2) {
-            l_sum[r] += x[r];
-            l_sum[r + 1] += x[r + 1];
-            l_rnd[r] += __uint_as_float(w[r / 2] << 16);
-            l_rnd[r + 1] += __uint_as_float(w[r / 2] & 0xFFFF0000u);
-          }
+        for (int r = 0; r < RH; r += 2) {
+          const f32x2 old = f2_pack(l_sum[r], l_sum[r + 1]), v = f2_pack(x[r], x[r + 1]);
+          f2_unpack(FP8 ? f2_fma(v, f2_pack(down, down), old) : f2_add(v, old), l_sum[r], l_sum[r + 1]);
+          if constexpr (!FP8)
+            f2_unpack(f2_add(bf16x2_to_f2(w[r / 2]), f2_pack(l_rnd[r], l_rnd[r + 1])), l_rnd[r], l_rnd[r + 1]);
         }
       }
       if (!ok) break;
@@ -876,7 +891,7 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
         const float l = lred[rr] + lred[NT + rr] + lred[2 * NT + rr] + lred[3 * NT + rr];
         const float ln = FP8 ? l : lred[4 * NT + rr] + lred[5 * NT + rr] + lred[6 * NT + rr] + lred[7 * NT + rr];
         if (i < rows) {
-          const float lse = l > 0.f ? (sm_m[rr] + log2f(l)) * kLn2 : -INFINITY;
+          const float lse = l > 0.f ? (log2f(l) - sm_nm[rr]) * kLn2 : -INFINITY;
           if (part >= 0) a.lse_part[(long long)part * NT + rr] = lse;
           else if (a.lse) a.lse[(long long)b * a.M + R0 + i] = lse;
         }
