@@ -47,6 +47,8 @@ namespace pda {
 
 struct LatentArgs {
   const uint16_t* q;  // bf16 [B, M, R + rope_dim], M = q_len * H
+  const uint8_t* latent_pages;
+  const uint16_t* rope_pages;
   const uint8_t* scales;
   const int32_t* page_table;
   const int32_t* kv_lens;
@@ -178,6 +180,10 @@ struct LatentCfg {
   // keeps the second term's smallest step 2^18 below the largest weight.
   static constexpr float HEAD = FP8 ? 4.f : 0.f;
 };
+
+__device__ __forceinline__ void l2_prefetch(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 
 // Loads `box` tokens from token group `group` on, of every token the 128-byte
 // columns from `col` on (make_tokens_map).
@@ -413,9 +419,33 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
         if (t >= d.first + d.n || lane >= segments(t)) return 0;
         return __ldg(pt + ((t * kTile + lane * seg_rows) >> a.log2_page));
       };
+      // The rotated parts go first (their slot is free as soon as S^T is): they are
+      // multiplied while the latents are on their way. (Overlay: their slot holds
+      // the weights until O^T is done.)
+      auto load_rope = [&](int nseg, int row) {
+        const int rs = g % C::R_SLOTS;
+        if (g >= C::R_SLOTS)
+          ok = __all_sync(FULL, wait_or_abort(&rempty[rs], ((g / C::R_SLOTS) - 1) & 1, abort_flag, a.err));
+        if (!ok) return false;
+        if (lane == 0) mbar_arrive_expect_tx(&rfull[rs], (uint32_t)(nseg * seg_rows) * 128u);
+        __syncwarp();
+        if (lane < nseg)
+          tma_load_2d(sbase + C::OFF_ROPE + rs * C::ROPE_SLOT + lane * seg_rows * 128, &map_r, 0, row, &rfull[rs]);
+        return true;
+      };
       int pid = page_of(d.first), pid_next = page_of(d.first + 1);
       for (int t = d.first; ok && t < d.first + d.n; ++t, ++g) {
         const int nseg = segments(t);
+        // A team of several CTAs: the next tile's segments into L2, by one of them:
+        // the copies, issued when shared memory is free, then find them there (74
+        // sequences of 8192 tokens, 128 heads: 235 -> 216 us). A CTA by itself is
+        // bound by HBM, and slower with it (148 sequences, 64 heads: 255 -> 268 us).
+        if (a.row_tiles > 1 && t + 1 < d.first + d.n && lane < segments(t + 1) && (unsigned)pid_next < (unsigned)a.num_pages &&
+            (t % a.row_tiles) == rt) {
+          const long long next = (long long)pid_next * a.page_size + (((t + 1) * kTile + lane * seg_rows) & (a.page_size - 1));
+          l2_prefetch(a.latent_pages + next * (FP8 ? R : 2 * R), seg_rows * (FP8 ? R : 2 * R));
+          l2_prefetch(a.rope_pages + next * a.rope_dim, seg_rows * a.rope_dim * 2);
+        }
         if ((unsigned)pid >= (unsigned)a.num_pages) {
           record_error_at(a.err, kErrBadPage);
           pid = 0;
@@ -423,6 +453,7 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
         const int row = pid * a.page_size + ((t * kTile + lane * seg_rows) & (a.page_size - 1));
         pid = pid_next;
         pid_next = page_of(t + 2);
+        if (!C::OVERLAY && !load_rope(nseg, row)) break;
 #pragma unroll 1
         for (int k = 0; k < C::UPT; ++k, ++blk) {
           const int sl = blk % C::SLOTS;
@@ -440,15 +471,7 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
                         FP8 ? 0 : 2 * k, row >> 3, &full[sl]);
         }
         if (!ok) break;
-        const int rs = g % C::R_SLOTS;
-        if (g >= C::R_SLOTS) {
-          ok = __all_sync(FULL, wait_or_abort(&rempty[rs], ((g / C::R_SLOTS) - 1) & 1, abort_flag, a.err));
-          if (!ok) break;
-        }
-        if (lane == 0) mbar_arrive_expect_tx(&rfull[rs], (uint32_t)(nseg * seg_rows) * 128u);
-        __syncwarp();
-        if (lane < nseg)
-          tma_load_2d(sbase + C::OFF_ROPE + rs * C::ROPE_SLOT + lane * seg_rows * 128, &map_r, 0, row, &rfull[rs]);
+        if (C::OVERLAY && !load_rope(nseg, row)) break;
       }
     }
     if (!ok) {
@@ -487,6 +510,25 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
           if (g >= 2) ok = agreed(wait_or_abort(&p_ready[bb], ((g - 2) >> 1) & 1, abort_flag, a.err));
           const uint32_t dt = tmem + C::COL_S + bb * C::SN;
           const uint64_t q0 = umma_desc(sbase + C::OFF_Q, 16, 1024, kSw128);
+          // bf16: into the columns of the latents' product, whichever comes first
+          auto rope_product = [&]() {
+            const int rs = g % C::R_SLOTS;
+            ok = ok && agreed(wait_or_abort(&rfull[rs], (g / C::R_SLOTS) & 1, abort_flag, a.err));
+            if (!ok) return false;
+            tmem_fence_after();
+            if (leader) {
+              constexpr uint32_t idesc = umma_idesc_bf16(128, NT, false, false);
+              const uint64_t ra = umma_desc(sbase + C::OFF_ROPE + rs * C::ROPE_SLOT, 16, 1024, kSw128);
+              const uint64_t qb = q0 + (C::Q_ROPE >> 4);
+#pragma unroll
+              for (int s = 0; s < 4; ++s)
+                umma_f16(FP8 ? dt + C::N1 : dt, ra + 2 * s, qb + 2 * s, idesc, C::OVERLAY || s > 0);
+              if constexpr (!C::OVERLAY) umma_commit(&rempty[rs]);
+            }
+            __syncwarp();
+            return true;
+          };
+          if (!C::OVERLAY && !rope_product()) break;
           if constexpr (FP8) {
             const int sl = blk % C::SLOTS;
             ok = ok && agreed(wait_or_abort(&full[sl], (blk / C::SLOTS) & 1, abort_flag, a.err) &&
@@ -518,25 +560,14 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
 #pragma unroll
                 for (int s = 0; s < 8; ++s)
                   umma_f16(dt, ca + (((s >> 2) * 1024 + (s & 3) * 32) >> 4),
-                           qb + (((s >> 2) * (NT * 128) + (s & 3) * 32) >> 4), idesc, k > 0 || s > 0);
+                           qb + (((s >> 2) * (NT * 128) + (s & 3) * 32) >> 4), idesc, !C::OVERLAY || k > 0 || s > 0);
               }
               __syncwarp();
             }
+            if (!ok) break;
           }
-          const int rs = g % C::R_SLOTS;
-          ok = agreed(ok && wait_or_abort(&rfull[rs], (g / C::R_SLOTS) & 1, abort_flag, a.err));
-          if (!ok) break;
-          tmem_fence_after();
-          if (leader) {
-            constexpr uint32_t idesc = umma_idesc_bf16(128, NT, false, false);
-            const uint64_t ra = umma_desc(sbase + C::OFF_ROPE + rs * C::ROPE_SLOT, 16, 1024, kSw128);
-            const uint64_t qb = q0 + (C::Q_ROPE >> 4);
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-              umma_f16(FP8 ? dt + C::N1 : dt, ra + 2 * s, qb + 2 * s, idesc, !FP8 || s > 0);
-            if constexpr (!C::OVERLAY) umma_commit(&rempty[rs]);
-            umma_commit(&s_full[bb]);
-          }
+          if (C::OVERLAY && !rope_product()) break;
+          if (leader) umma_commit(&s_full[bb]);
           __syncwarp();
           issued = g + 1;
         }

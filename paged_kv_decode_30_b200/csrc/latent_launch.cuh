@@ -15,6 +15,8 @@ cudaError_t launch_latent(const LatentCall& c, cudaStream_t stream) {
   const pda_latent_params& p = *c.p;
   LatentArgs a{};
   a.q = static_cast<const uint16_t*>(c.q);
+  a.latent_pages = static_cast<const uint8_t*>(c.latent_pages);
+  a.rope_pages = static_cast<const uint16_t*>(c.rope_pages);
   a.scales = static_cast<const uint8_t*>(p.latent_scales);
   a.page_table = c.page_table;
   a.kv_lens = c.kv_lens;
