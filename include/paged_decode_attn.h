@@ -407,7 +407,7 @@ typedef struct {
  * latent       device, bf16 [total_rows, latent_dim], row stride latent_stride.
  * rope         device, bf16 [total_rows, rope_dim], row stride rope_stride.
  * row_offsets  device, int32 [B + 1], not decreasing. Rows outside
- *              [row_offsets[0], row_offsets[B]) are not read.
+ *              [row_offsets[0], row_offsets[B]) are not used.
  * page_table   device, int32 [B, max_pages_per_seq]; the pages covering the
  *              new positions must already be assigned.
  * kv_lens      device, int32 [B]: lengths before the append (read only).

@@ -539,11 +539,9 @@ def paged_latent_gather(latent_pages, rope_pages, page_table, row_offsets, *, to
         if total_rows is None:
             raise ValueError("total_rows is needed to allocate the outputs")
         if latent is None:
-            latent = torch.empty((total_rows, _sizes("latent_pages", latent_pages, 3)[2]),
-                                 dtype=torch.bfloat16, device=latent_pages.device)
+            latent = rope_pages.new_empty((total_rows, _sizes("latent_pages", latent_pages, 3)[2]))
         if rope is None:
-            rope = torch.empty((total_rows, _sizes("rope_pages", rope_pages, 3)[2]),
-                               dtype=torch.bfloat16, device=latent_pages.device)
+            rope = rope_pages.new_empty((total_rows, _sizes("rope_pages", rope_pages, 3)[2]))
     p = _latent_rows(latent, rope, row_offsets, page_table, starts, latent_pages, rope_pages,
                      latent_scales)
     st = load().paged_latent_gather(latent_pages.data_ptr(), rope_pages.data_ptr(),
@@ -573,13 +571,13 @@ def paged_latent_decode(q, latent_pages, rope_pages, page_table, kv_lens, *, sca
     _check("kv_lens", kv_lens, torch.int32, (B,), dev)
     handle = _current_stream(dev, stream)
     if out is None:
-        out = torch.empty((B, q_len, H, width), dtype=torch.bfloat16, device=dev)
+        out = q.new_empty((B, q_len, H, width))
     else:
         _check("out", out, torch.bfloat16, (B, q_len, H, width), dev)
     if lse is not None:
         _check("lse", lse, torch.float32, (B, q_len, H), dev)
     elif with_lse:
-        lse = torch.empty((B, q_len, H), dtype=torch.float32, device=dev)
+        lse = q.new_empty((B, q_len, H), dtype=torch.float32)
     p = PdaLatentParams(B, q_len, H, width, rope_dim, page, max_pages, num_pages, scale,
                         causal_offset, window, kv_dtype, flags, _ptr(latent_scales), None, 0)
     if workspace is None and not library_workspace:
@@ -587,7 +585,7 @@ def paged_latent_decode(q, latent_pages, rope_pages, page_table, kv_lens, *, sca
         if need == ctypes.c_size_t(-1).value:
             need = 0  # the call below says what is wrong
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = q.new_empty(need, dtype=torch.uint8)
     if workspace is not None:
         p.workspace = workspace.data_ptr()
         p.workspace_bytes = workspace.nbytes
@@ -622,13 +620,13 @@ def latent_prefill_attn(q, kv, k_rope, q_offsets, kv_offsets, *, scale,
     _check("kv_offsets", kv_offsets, torch.int32, (B + 1,), dev)
     handle = _current_stream(dev, stream)
     if out is None:
-        out = torch.empty((total_q, H, D), dtype=torch.bfloat16, device=dev)
+        out = q.new_empty((total_q, H, D))
     else:
         _check("out", out, torch.bfloat16, (total_q, H, D), dev)
     if lse is not None:
         _check("lse", lse, torch.float32, (total_q, H), dev)
     elif with_lse:
-        lse = torch.empty((total_q, H), dtype=torch.float32, device=dev)
+        lse = q.new_empty((total_q, H), dtype=torch.float32)
     p = PdaLatentPrefillParams(B, total_q, total_kv, total_q if max_q_len is None else max_q_len, H,
                                D, width - D, _row_stride(k_rope), scale, causal_offset, window)
     st = lib.latent_prefill_attn(q.data_ptr(), kv.data_ptr(), k_rope.data_ptr(), q_offsets.data_ptr(),

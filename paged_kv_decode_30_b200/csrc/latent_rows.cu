@@ -3,10 +3,10 @@
 //
 // Both directions move each row once and compute next to nothing, so they are
 // bound by HBM for many rows and by latency for few. A warp owns RB
-// consecutive ragged rows: lanes look up the slots of the RB rows at the same
-// time (owner by binary search over row_offsets, then page table), then the
-// warp streams the rows through registers, 16 bytes a lane and access, with
-// the loads of several rows in flight before the first store.
+// consecutive ragged rows: it looks up their slots at the same time (the owner
+// from row_offsets, then the page table; rows to be written are loaded beside
+// that), then streams the rows through registers, 16 bytes a lane and access,
+// with the loads of several rows in flight before the first store.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -37,19 +37,53 @@ struct RowsArgs {
 
 constexpr int kScaleBias = 127, kScaleMin = -30, kScaleMax = 30;
 
-// Slot (row of the flattened pools) of ragged row `row`; -1 if no sequence
-// owns it or (recorded) its position or page is out of range.
-__device__ __forceinline__ long long slot_of_row(const RowsArgs& a, int row) {
-  if (row >= a.total) return -1;
-  int lo = 0, hi = a.B + 1;  // the last b with row_offsets[b] <= row lies in [lo - 1, hi)
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(a.row_offsets + mid) <= row) lo = mid + 1;
-    else hi = mid;
+// The sequence of each of the warp's RB rows r0, r0 + 1, ...: lane u < RB gets
+// row r0 + u's, the last b with row_offsets[b] <= row (-1: none; B: behind the
+// last). Up to 1024 sequences the warp loads 32 offsets at a time and counts by
+// votes, two loads deep; beyond, each lane searches by halving.
+template <int RB>
+__device__ __forceinline__ int find_owners(const RowsArgs& a, int r0, int lane) {
+  constexpr unsigned FULL = 0xFFFFFFFFu;
+  const int n = a.B + 1;
+  int b = -1;
+  if (n <= 32) {
+    const int v = lane < n ? __ldg(a.row_offsets + lane) : 0x7FFFFFFF;
+#pragma unroll
+    for (int u = 0; u < RB; ++u) {
+      const int c = __popc(__ballot_sync(FULL, lane < n && v <= r0 + u));
+      if (lane == u) b = c - 1;
+    }
+  } else if (n <= 1024) {
+    const int step = (n + 31) / 32, at = lane * step;
+    const int v = at < n ? __ldg(a.row_offsets + at) : 0x7FFFFFFF;
+    int k[RB], w[RB];
+#pragma unroll
+    for (int u = 0; u < RB; ++u) {
+      k[u] = max(__popc(__ballot_sync(FULL, at < n && v <= r0 + u)) - 1, 0) * step;
+      w[u] = lane < step && k[u] + lane < n ? __ldg(a.row_offsets + k[u] + lane) : 0x7FFFFFFF;
+    }
+#pragma unroll
+    for (int u = 0; u < RB; ++u) {
+      const int c = __popc(__ballot_sync(FULL, lane < step && k[u] + lane < n && w[u] <= r0 + u));
+      if (lane == u) b = k[u] + c - 1;
+    }
+  } else if (lane < RB) {
+    int lo = 0, hi = n;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(a.row_offsets + mid) <= r0 + lane) lo = mid + 1;
+      else hi = mid;
+    }
+    b = lo - 1;
   }
-  const int b = lo - 1;
-  if (b < 0 || b >= a.B) return -1;
-  const long long t = (long long)row - __ldg(a.row_offsets + b);
+  return b;
+}
+
+// Slot (row of the flattened pools) of ragged row `row` of sequence b; -1 if no
+// sequence owns it or (recorded) its position or page is out of range.
+__device__ __forceinline__ long long slot_of_row(const RowsArgs& a, long long row, int b) {
+  if (row >= a.total || b < 0 || b >= a.B) return -1;
+  const long long t = row - __ldg(a.row_offsets + b);
   const int start = a.starts ? __ldg(a.starts + b) : 0;
   const long long pos = start + t;
   int page = -1;
@@ -114,16 +148,26 @@ __device__ __forceinline__ uint4 dequantise8(const uint2& c, float scale) {
 }
 
 template <int R, bool FP8, bool WRITE, int RB>
-__global__ void __launch_bounds__(256) latent_rows_kernel(const RowsArgs a) {
+__global__ void __launch_bounds__(256, 4) latent_rows_kernel(const RowsArgs a) {
   constexpr unsigned FULL = 0xFFFFFFFFu;
   constexpr int C = R / 256;           // 16-byte bf16 pieces of a row per lane
   constexpr int U = RB < 4 ? RB : 4;   // rows in flight
   const int lane = threadIdx.x & 31;
-  const long long warp = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const long long nwarps = (long long)gridDim.x * 8;
-  for (long long r0 = warp * RB; r0 < a.total; r0 += nwarps * RB) {
-    const long long mine = lane < RB ? slot_of_row(a, (int)min(r0 + lane, (long long)a.total)) : -1;
-    if (__ballot_sync(FULL, mine >= 0) == 0) continue;
+  const long long r0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * RB;
+  if (r0 < a.total) {
+    uint4 v[U][C];  // bf16 pieces of U rows
+    auto load_rows = [&](int u0) {  // of the ragged side: needs no slot
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint4* src = reinterpret_cast<const uint4*>(a.latent + min(r0 + u0 + u, a.total - 1ll) * a.latent_stride);
+#pragma unroll
+        for (int c = 0; c < C; ++c) v[u][c] = src[lane + 32 * c];
+      }
+    };
+    if constexpr (WRITE) load_rows(0);  // beside the lookups
+    const int owner = find_owners<RB>(a, (int)r0, lane);
+    const long long mine = lane < RB ? slot_of_row(a, r0 + lane, owner) : -1;
+    if (__ballot_sync(FULL, mine >= 0) == 0) return;
     // rope parts: (row, 16-byte piece) pairs over the lanes
     const int log2_pieces = a.rope_dim == 64 ? 3 : 2;
     constexpr int RP = (RB * 8 + 31) / 32;
@@ -141,17 +185,15 @@ __global__ void __launch_bounds__(256) latent_rows_kernel(const RowsArgs a) {
 #pragma unroll
     for (int u0 = 0; u0 < RB; u0 += U) {
       long long slot[U];
-      uint4 v[U][C];  // bf16 pieces
       uint2 q[U][C];  // e4m3 pieces
       uint32_t sb[U];
+      if (WRITE && u0 > 0) load_rows(u0);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         slot[u] = __shfl_sync(FULL, mine, u0 + u);
         if (slot[u] < 0) continue;
         if constexpr (WRITE) {
-          const uint4* src = reinterpret_cast<const uint4*>(a.latent + (r0 + u0 + u) * a.latent_stride);
-#pragma unroll
-          for (int c = 0; c < C; ++c) v[u][c] = src[lane + 32 * c];
+          // loaded already
         } else if constexpr (FP8) {
           const uint2* src = reinterpret_cast<const uint2*>(a.latent_pages + slot[u] * R);
 #pragma unroll
@@ -209,8 +251,7 @@ void launch_rows(const RowsArgs& a, int sms, cudaStream_t stream) {
   if (a.total <= sms * 16) {
     latent_rows_kernel<R, FP8, WRITE, 1><<<(a.total + 7) / 8, 256, 0, stream>>>(a);
   } else {
-    const int want = (a.total + 63) / 64, most = sms * 8;
-    latent_rows_kernel<R, FP8, WRITE, 8><<<want < most ? want : most, 256, 0, stream>>>(a);
+    latent_rows_kernel<R, FP8, WRITE, 8><<<(a.total + 63) / 64, 256, 0, stream>>>(a);
   }
 }
 
