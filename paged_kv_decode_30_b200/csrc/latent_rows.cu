@@ -147,6 +147,19 @@ __device__ __forceinline__ uint4 dequantise8(const uint2& c, float scale) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Rows of large calls pass the caches by (each byte is used once): 77 k FP8 rows
+// gathered in 24.3 us instead of 26.1.
+template <bool STREAM, typename T>
+__device__ __forceinline__ T get(const T* p) {
+  if constexpr (STREAM) return __ldcs(p);
+  else return *p;
+}
+template <bool STREAM, typename T>
+__device__ __forceinline__ void put(T* p, const T& v) {
+  if constexpr (STREAM) __stcs(p, v);
+  else *p = v;
+}
+
 template <int R, bool FP8, bool WRITE, int RB>
 __global__ void __launch_bounds__(256, 4) latent_rows_kernel(const RowsArgs a) {
   constexpr unsigned FULL = 0xFFFFFFFFu;
@@ -161,7 +174,7 @@ __global__ void __launch_bounds__(256, 4) latent_rows_kernel(const RowsArgs a) {
       for (int u = 0; u < U; ++u) {
         const uint4* src = reinterpret_cast<const uint4*>(a.latent + min(r0 + u0 + u, a.total - 1ll) * a.latent_stride);
 #pragma unroll
-        for (int c = 0; c < C; ++c) v[u][c] = src[lane + 32 * c];
+        for (int c = 0; c < C; ++c) v[u][c] = get<(RB > 1)>(src + lane + 32 * c);
       }
     };
     if constexpr (WRITE) load_rows(0);  // beside the lookups
@@ -197,12 +210,12 @@ __global__ void __launch_bounds__(256, 4) latent_rows_kernel(const RowsArgs a) {
         } else if constexpr (FP8) {
           const uint2* src = reinterpret_cast<const uint2*>(a.latent_pages + slot[u] * R);
 #pragma unroll
-          for (int c = 0; c < C; ++c) q[u][c] = src[lane + 32 * c];
+          for (int c = 0; c < C; ++c) q[u][c] = get<(RB > 1)>(src + lane + 32 * c);
           sb[u] = a.scales[slot[u]];
         } else {
           const uint4* src = reinterpret_cast<const uint4*>(a.latent_pages + slot[u] * R * 2);
 #pragma unroll
-          for (int c = 0; c < C; ++c) v[u][c] = src[lane + 32 * c];
+          for (int c = 0; c < C; ++c) v[u][c] = get<(RB > 1)>(src + lane + 32 * c);
         }
       }
 #pragma unroll
@@ -216,7 +229,7 @@ __global__ void __launch_bounds__(256, 4) latent_rows_kernel(const RowsArgs a) {
           const float inv = exp2_int(-e);
           uint2* dst = reinterpret_cast<uint2*>(a.latent_pages + slot[u] * R);
 #pragma unroll
-          for (int c = 0; c < C; ++c) dst[lane + 32 * c] = quantise8(v[u][c], inv);
+          for (int c = 0; c < C; ++c) put<(RB > 1)>(dst + lane + 32 * c, quantise8(v[u][c], inv));
           if (lane == 0) a.scales[slot[u]] = (uint8_t)(e + kScaleBias);
         } else {
           uint4* dst = reinterpret_cast<uint4*>(
@@ -225,10 +238,10 @@ __global__ void __launch_bounds__(256, 4) latent_rows_kernel(const RowsArgs a) {
           if constexpr (FP8) {
             const float s = exp2_int(min(max((int)sb[u] - kScaleBias, kScaleMin), kScaleMax));
 #pragma unroll
-            for (int c = 0; c < C; ++c) dst[lane + 32 * c] = dequantise8(q[u][c], s);
+            for (int c = 0; c < C; ++c) put<(RB > 1)>(dst + lane + 32 * c, dequantise8(q[u][c], s));
           } else {
 #pragma unroll
-            for (int c = 0; c < C; ++c) dst[lane + 32 * c] = v[u][c];
+            for (int c = 0; c < C; ++c) put<(RB > 1)>(dst + lane + 32 * c, v[u][c]);
           }
         }
       }
@@ -246,12 +259,13 @@ __global__ void __launch_bounds__(256, 4) latent_rows_kernel(const RowsArgs a) {
 template <int R, bool FP8, bool WRITE>
 void launch_rows(const RowsArgs& a, int sms, cudaStream_t stream) {
   // Few rows: one a warp, so that the lookups of all rows run side by side.
-  // Many: eight a warp, so that a lookup's chain of dependent loads is paid
-  // once for eight rows.
+  // Many: four a warp, so that a lookup's chain of dependent loads is paid once
+  // for four rows, and 64 or 128 bytes a lane are in flight (77 k FP8 rows: 24.3 us;
+  // eight a warp 25.0).
   if (a.total <= sms * 16) {
     latent_rows_kernel<R, FP8, WRITE, 1><<<(a.total + 7) / 8, 256, 0, stream>>>(a);
   } else {
-    latent_rows_kernel<R, FP8, WRITE, 8><<<(a.total + 63) / 64, 256, 0, stream>>>(a);
+    latent_rows_kernel<R, FP8, WRITE, 4><<<(a.total + 31) / 32, 256, 0, stream>>>(a);
   }
 }
 
