@@ -261,13 +261,31 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
   int* sums = reinterpret_cast<int*>(smem + C::OFF_MISC + 16);  // [WARPS]
   LatentItem* items = reinterpret_cast<LatentItem*>(smem + C::OFF_ITEM);
 
-  // This thread's sequences' share of the line (the loads go out first).
+  // The sequences' shares of the line (the loads go out first). Up to 128: the
+  // schedule warp has them to itself, four consecutive ones a lane; more: every
+  // warp adds up one chunk, and the schedule warp looks into the chunks it needs.
+  constexpr int K = 4;
+  const bool few = a.B <= 32 * K;
   const int chunk = (a.B + C::WARPS - 1) / C::WARPS;
   int w_sum = 0;  // (the host refuses calls of 2^31 tiles or more)
-  for (int b = warp * chunk + lane; b < min(a.B, (warp + 1) * chunk); b += 32) {
-    const int L = __ldg(a.kv_lens + b);
-    w_sum += latent_weight(a, L);
+  int lens[K], wts[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) lens[k] = wts[k] = 0;
+  auto share_of = [&](int L) {
     if (blockIdx.x == 0 && (L < 0 || L > (a.max_pages << a.log2_page))) record_error_at(a.err, kErrBadPage);
+    return latent_weight(a, L);
+  };
+  if (!few) {
+    for (int b = warp * chunk + lane; b < min(a.B, (warp + 1) * chunk); b += 32) w_sum += share_of(__ldg(a.kv_lens + b));
+  } else if (warp == 3) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (lane * K + k < a.B) lens[k] = __ldg(a.kv_lens + lane * K + k);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (lane * K + k < a.B) wts[k] = share_of(lens[k]);
+      w_sum += wts[k];
+    }
   }
   if (tid < C::BARS) {
     uint64_t* bar = full + tid;
@@ -287,8 +305,10 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  w_sum = __reduce_add_sync(FULL, w_sum);
-  if (lane == 0) sums[warp] = w_sum;
+  if (!few) {
+    const int sum = __reduce_add_sync(FULL, w_sum);
+    if (lane == 0) sums[warp] = sum;
+  }
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
@@ -300,8 +320,8 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
     // The line's length and this team's range [s, e) of it (a line shorter than
     // the number of teams leaves the last ones idle, so that no range is empty);
     // then every sequence that overlaps the range becomes an item.
-    int upto = lane < C::WARPS ? sums[lane] : 0;  // up to and with warp `lane`'s chunk
-    const int own_sum = upto;
+    const int own_sum = few ? w_sum : lane < C::WARPS ? sums[lane] : 0;
+    int upto = own_sum;  // up to and with this lane's sequences, or chunk `lane`
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(FULL, upto, o);
@@ -363,9 +383,28 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
       }
       ++j;
     };
-    // the chunk that holds unit s, then on to the range's end
-    int w = __ffs(__ballot_sync(FULL, s < e && upto > s)) - 1;
-    int at = w >= 0 ? __shfl_sync(FULL, upto - own_sum, w) : 0;  // where the sequences looked at next begin
+    if (few) {
+      int begin[K], hits = 0;
+      begin[0] = upto - own_sum;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (k > 0) begin[k] = begin[k - 1] + wts[k - 1];
+        if (wts[k] > 0 && begin[k] < e && begin[k] + wts[k] > s && s < e) hits |= 1 << k;
+      }
+      unsigned lanes = __ballot_sync(FULL, hits != 0);
+      while (lanes && ok) {
+        const int src = __ffs(lanes) - 1, mask = __shfl_sync(FULL, hits, src);
+        lanes &= lanes - 1;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+          if (ok && (mask >> k & 1))
+            publish(src * K + k, __shfl_sync(FULL, lens[k], src), __shfl_sync(FULL, begin[k], src),
+                    __shfl_sync(FULL, wts[k], src));
+      }
+    }
+    // more: the chunk that holds unit s, then on to the range's end
+    int w = few ? -1 : __ffs(__ballot_sync(FULL, s < e && upto > s)) - 1;
+    int at = __shfl_sync(FULL, upto - own_sum, max(w, 0));  // where the sequences looked at next begin
     for (; w >= 0 && w < C::WARPS && ok && at < e; ++w) {
       const int b1 = min(a.B, (w + 1) * chunk);
       for (int b0 = w * chunk; b0 < b1 && ok && at < e; b0 += 32) {
