@@ -1046,7 +1046,8 @@ __global__ void __launch_bounds__(kMergeThreads, 2) latent_merge_kernel(const La
   int n_few = 0, n_many = 0;
   {
     const int2 c = tid < a.teams ? a.cut[tid] : make_int2(-1, 0);
-    const int parts = c.x >= 0 ? c.y - tid + 1 : 0;
+    // (a schedule that gave up may have left anything)
+    const int parts = c.x >= 0 && c.x < a.B && c.y > tid && c.y < a.teams ? c.y - tid + 1 : 0;
     const bool few = parts > 0 && parts <= kMergeFew, many = parts > kMergeFew;
     const unsigned f = __ballot_sync(FULL, few), m = __ballot_sync(FULL, many);
     if (lane == 0 && warp < kMergeTeams / 32) warp_n[warp] = make_int2(__popc(f), __popc(m));

@@ -265,7 +265,7 @@ void launch_rows(const RowsArgs& a, int sms, cudaStream_t stream) {
   if (a.total <= sms * 16) {
     latent_rows_kernel<R, FP8, WRITE, 1><<<(a.total + 7) / 8, 256, 0, stream>>>(a);
   } else {
-    latent_rows_kernel<R, FP8, WRITE, 4><<<(a.total + 31) / 32, 256, 0, stream>>>(a);
+    latent_rows_kernel<R, FP8, WRITE, 4><<<(unsigned)((a.total + 31ll) / 32), 256, 0, stream>>>(a);
   }
 }
 
