@@ -484,9 +484,16 @@ def _latent_pools(latent_pages, rope_pages, latent_scales, page_table):
     rope_dim = _sizes("rope_pages", rope_pages, 3)[2]
     table = _sizes("page_table", page_table, 2)
     fp8 = latent_pages.dtype is torch.uint8
-    _check("latent_pages", latent_pages, torch.uint8 if fp8 else torch.bfloat16, pools, dev)
-    _check("rope_pages", rope_pages, torch.bfloat16, (num_pages, page, rope_dim), dev)
-    _check("page_table", page_table, torch.int32, table, dev)
+    # (one expression for what fits, the checks one by one for what does not: these
+    # calls are short, and a Python call a tensor shows)
+    if not ((fp8 or latent_pages.dtype is torch.bfloat16) and rope_pages.dtype is torch.bfloat16
+            and page_table.dtype is torch.int32 and rope_pages.shape == (num_pages, page, rope_dim)
+            and rope_pages.device == dev and page_table.device == dev
+            and latent_pages.is_contiguous() and rope_pages.is_contiguous()
+            and page_table.is_contiguous()):
+        _check("latent_pages", latent_pages, torch.uint8 if fp8 else torch.bfloat16, pools, dev)
+        _check("rope_pages", rope_pages, torch.bfloat16, (num_pages, page, rope_dim), dev)
+        _check("page_table", page_table, torch.int32, table, dev)
     if fp8:
         if latent_scales is None:
             raise ValueError("uint8 latent_pages need latent_scales")
@@ -501,9 +508,14 @@ def _latent_rows(latent, rope, row_offsets, page_table, starts, latent_pages, ro
     dev, (num_pages, page, width), rope_dim, (batch, max_pages), kv_dtype = _latent_pools(
         latent_pages, rope_pages, latent_scales, page_table)
     rows = _sizes("latent", latent, 2)[0]
-    _check("latent", latent, torch.bfloat16, (rows, width), dev, rows=True)
-    _check("rope", rope, torch.bfloat16, (rows, rope_dim), dev, rows=True)
-    _check("row_offsets", row_offsets, torch.int32, (batch + 1,), dev)
+    if not (latent.dtype is torch.bfloat16 and rope.dtype is torch.bfloat16
+            and row_offsets.dtype is torch.int32 and latent.shape == (rows, width)
+            and rope.shape == (rows, rope_dim) and row_offsets.shape == (batch + 1,)
+            and latent.device == dev and rope.device == dev and row_offsets.device == dev
+            and latent.stride(1) == 1 and rope.stride(1) == 1 and row_offsets.is_contiguous()):
+        _check("latent", latent, torch.bfloat16, (rows, width), dev, rows=True)
+        _check("rope", rope, torch.bfloat16, (rows, rope_dim), dev, rows=True)
+        _check("row_offsets", row_offsets, torch.int32, (batch + 1,), dev)
     if starts is not None:
         _check("kv_lens / starts", starts, torch.int32, (batch,), dev)
     return PdaLatentRowsParams(batch, rows, width, rope_dim, page, max_pages, num_pages, kv_dtype,
