@@ -176,9 +176,10 @@ struct LatentCfg {
   static constexpr int TMEM_COLS = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
   static_assert(COLS <= 512 && SLOTS >= UPT && SMEM_ALLOC <= 227 * 1024, "capacity");
   static_assert(BLK % 1024 == 0 && Q_BLK % 1024 == 0 && Q_BYTES % 1024 == 0 && P_BYTES % 1024 == 0, "alignment");
-  // Weights are at most 2^8 (e4m3 holds 448). FP8 starts them at 2^4, which
-  // keeps the second term's smallest step 2^18 below the largest weight.
-  static constexpr float HEAD = FP8 ? 4.f : 0.f;
+  // Weights are at most 2^8 (e4m3 holds 448). FP8 starts them at 2^6: what the
+  // second term cannot hold, half its smallest step, is then 2^-20 of the row's
+  // largest weight, and a maximum that grows by less than 2^2 still moves nothing.
+  static constexpr float HEAD = FP8 ? 6.f : 0.f;
 };
 
 __device__ __forceinline__ void l2_prefetch(const void* p, uint32_t bytes) {
@@ -726,20 +727,17 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
 #pragma unroll
           for (int k = 0; k < E; ++k) mx = fmaxf(mx, fabsf(f[k]));
           mx = redux_max(mx);
-          const int e2 = mx > 0.f && mx < INFINITY ? min(7 - ilogbf(mx), 120) : 0;
-          const float up = ldexpf(1.f, e2);
-          if (lane == 0) sm_cs[nrow] = ldexpf(a.scale_log2, -e2);
+          // 2^e2 from the exponent field of mx (0 for a row of zeros; within 2^+-120)
+          const int e2 = mx > 0.f ? min(max(134 - (int)(__float_as_uint(mx) >> 23), -120), 120) : 0;
+          const float up = __int_as_float((127 + e2) << 23);
+          if (lane == 0) sm_cs[nrow] = a.scale_log2 * __int_as_float((127 - e2) << 23);
           uint32_t hw[E / 4], lw[E / 4];
 #pragma unroll
-          for (int x = 0; x < E / 4; ++x) {
-            hw[x] = lw[x] = 0;
-#pragma unroll
-            for (int k = 0; k < 4; k += 2) {
-              const float x0 = f[4 * x + k] * up, x1 = f[4 * x + k + 1] * up;
-              const uint32_t h2 = f32x2_to_e4m3x2(x0, x1);
-              hw[x] |= h2 << (8 * k);
-              lw[x] |= f32x2_to_e4m3x2((x0 - e4m3_to_f32(h2)) * 16.f, (x1 - e4m3_to_f32(h2 >> 8)) * 16.f) << (8 * k);
-            }
+          for (int x = 0; x < E / 4; ++x) {  // (bf16's 8 bits times 2^e2 fit f16, in which the split works)
+            const uint32_t s01 = e4m3_split2(f[4 * x] * up, f[4 * x + 1] * up);
+            const uint32_t s23 = e4m3_split2(f[4 * x + 2] * up, f[4 * x + 3] * up);
+            hw[x] = __byte_perm(s01, s23, 0x5410);
+            lw[x] = __byte_perm(s01, s23, 0x7632);
           }
           const int rh = 2 * r0 + rr, rl = rh + RH, el = lane * E;
           uint8_t* blk_base = qs + (el >> 7) * C::Q_BLK;

@@ -149,9 +149,8 @@ def check(got_out, got_lse, ref, width, what="", fp8=None):
       |d out| <= U16 * (sum p |v| + |out|) + U16 * |out|,
     and fp32 accumulation adds at most about width * U32 of the same sums. FP8 (fp8
     = (keys, max |v|)): the two-term weights also carry an absolute error of up to
-    2^-18 of the row's largest weight (half the smallest step of the second term,
-    2^-14, with the largest weight at 2^4 or more); over n keys, with random signs,
-    seven standard deviations of the sum are below 4 sqrt(n) 2^-18 max |v|.
+    2^-18 of the row's largest weight; over n keys, with random signs, seven
+    standard deviations of the sum are below 4 sqrt(n) 2^-18 max |v|.
     lse: a score is a sum of `width` products in fp32, off by at most width * U32 *
     scale * sum |q k|; exp2, log2 and the sum over keys add a few U32 of lse and
     2^-20; FP8 queries are split to within 2^-21 of their row's maximum."""
