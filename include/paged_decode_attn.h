@@ -479,7 +479,7 @@ typedef struct {
  *              value up-projection).
  * lse          device, fp32 [B, q_len, H], natural log; may be NULL.
  * Accumulation and softmax statistics are fp32; each weight enters the sum
- * over values with 8 significant bits (FP8 caches: or to 2^-20 of the row's
+ * over values with 8 significant bits (FP8 caches: or to 2^-18 of the row's
  * largest weight, whichever is coarser).
  *
  * Slots of a page past kv_lens[b] and keys no row may see are never weighted
