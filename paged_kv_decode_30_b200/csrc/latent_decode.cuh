@@ -107,6 +107,143 @@ struct LatentItem {
   int pad[3];
 };
 
+// The sequences' shares of the line, as a warp holds them. Up to 128 sequences
+// the schedule warp has them to itself, four consecutive ones a lane; more: every
+// warp adds up one chunk, and the schedule warp looks into the chunks it needs.
+struct LatentShares {
+  static constexpr int K = 4;
+  bool few;
+  int chunk, sum;          // sequences a warp; this lane's sum
+  int lens[K], wts[K];
+};
+
+template <int WARPS>
+__device__ __forceinline__ void latent_load_shares(const LatentArgs& a, LatentShares& sh, int warp, int lane,
+                                                   bool schedules) {
+  sh.few = a.B <= 32 * LatentShares::K;
+  sh.chunk = (a.B + WARPS - 1) / WARPS;
+  sh.sum = 0;  // (the host refuses calls of 2^31 tiles or more)
+#pragma unroll
+  for (int k = 0; k < LatentShares::K; ++k) sh.lens[k] = sh.wts[k] = 0;
+  auto share_of = [&](int L) {
+    if (blockIdx.x == 0 && (L < 0 || L > (a.max_pages << a.log2_page))) record_error_at(a.err, kErrBadPage);
+    return latent_weight(a, L);
+  };
+  if (!sh.few) {
+    for (int b = warp * sh.chunk + lane; b < min(a.B, (warp + 1) * sh.chunk); b += 32)
+      sh.sum += share_of(__ldg(a.kv_lens + b));
+  } else if (schedules) {
+#pragma unroll
+    for (int k = 0; k < LatentShares::K; ++k)
+      if (lane * LatentShares::K + k < a.B) sh.lens[k] = __ldg(a.kv_lens + lane * LatentShares::K + k);
+#pragma unroll
+    for (int k = 0; k < LatentShares::K; ++k) {
+      if (lane * LatentShares::K + k < a.B) sh.wts[k] = share_of(sh.lens[k]);
+      sh.sum += sh.wts[k];
+    }
+  }
+}
+
+// Walks the line (the whole schedule warp, after the block's barrier; sums: the
+// warps' chunk sums): its length, team `team`'s range [s, e) of it (a line shorter
+// than the number of teams leaves the last ones idle, so that no range is empty),
+// and publish(b, kv_len, t0, t1, whole, goes_on) for every sequence that overlaps
+// the range: its tiles [t0, t1), whether they are all, whether it goes on behind
+// the range. Stops once ok is false. Returns the cut sequence that starts in the
+// range (-1: none) and the team of its last tile.
+template <int WARPS, typename F>
+__device__ __forceinline__ int2 latent_schedule(const LatentArgs& a, const LatentShares& sh, const int* sums,
+                                                int team, int lane, const bool& ok, F publish) {
+  constexpr unsigned FULL = 0xFFFFFFFFu;
+  constexpr int K = LatentShares::K;
+  const int own_sum = sh.few ? sh.sum : lane < WARPS ? sums[lane] : 0;
+  int upto = own_sum;  // up to and with this lane's sequences, or chunk `lane`
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(FULL, upto, o);
+    if (lane >= o) upto += y;
+  }
+  const int total = __shfl_sync(FULL, upto, 31);
+  // the first `more` teams take share + 1 units, the rest share
+  const int teams = min(a.teams, total), share = total / teams, more = total - share * teams;
+  const int s = team < teams ? share * team + min(team, more) : total;
+  const int e = team < teams ? s + share + (team < more ? 1 : 0) : 0;
+  int cut_b = -1, cut_last = 0;  // the cut sequence that starts here and the unit of its last tile
+  auto found = [&](int b, int len, int begin, int w) {
+    const int t0 = max(s, begin) - begin, t1 = min(e, begin + w) - begin;
+    const bool whole = t0 == 0 && t1 == w;
+    if (t0 == 0 && !whole) {
+      cut_b = b;
+      cut_last = begin + w - 1;
+    }
+    publish(b, len, t0, t1, whole, begin + w > e);
+  };
+  if (sh.few) {
+    int begin[K], hits = 0;
+    begin[0] = upto - own_sum;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (k > 0) begin[k] = begin[k - 1] + sh.wts[k - 1];
+      if (sh.wts[k] > 0 && begin[k] < e && begin[k] + sh.wts[k] > s && s < e) hits |= 1 << k;
+    }
+    unsigned lanes = __ballot_sync(FULL, hits != 0);
+    while (lanes && ok) {
+      const int src = __ffs(lanes) - 1, mask = __shfl_sync(FULL, hits, src);
+      lanes &= lanes - 1;
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (ok && (mask >> k & 1))
+          found(src * K + k, __shfl_sync(FULL, sh.lens[k], src), __shfl_sync(FULL, begin[k], src),
+                __shfl_sync(FULL, sh.wts[k], src));
+    }
+  } else {
+    // the chunk that holds unit s, then on to the range's end
+    int w = __ffs(__ballot_sync(FULL, s < e && upto > s)) - 1;
+    int at = __shfl_sync(FULL, upto - own_sum, max(w, 0));  // where the sequences looked at next begin
+    for (; w >= 0 && w < WARPS && ok && at < e; ++w) {
+      const int b1 = min(a.B, (w + 1) * sh.chunk);
+      for (int b0 = w * sh.chunk; b0 < b1 && ok && at < e; b0 += 32) {
+        const int len = b0 + lane < b1 ? __ldg(a.kv_lens + b0 + lane) : 0;
+        const int wt = b0 + lane < b1 ? latent_weight(a, len) : 0;
+        int inc = wt;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(FULL, inc, o);
+          if (lane >= o) inc += y;
+        }
+        const int begin = at + inc - wt;
+        unsigned hit = __ballot_sync(FULL, wt > 0 && begin < e && begin + wt > s);
+        while (hit && ok) {
+          const int src = __ffs(hit) - 1;
+          hit &= hit - 1;
+          found(b0 + src, __shfl_sync(FULL, len, src), __shfl_sync(FULL, begin, src), __shfl_sync(FULL, wt, src));
+        }
+        at += __shfl_sync(FULL, inc, 31);
+      }
+    }
+  }
+  if (ok) publish(-1, 0, 0, 0, false, false);
+  const int wide = (share + 1) * more;
+  return make_int2(cut_b, cut_last < wide ? cut_last / (share + 1) : more + (cut_last - wide) / share);
+}
+
+// Item d: tiles [t0, t1) of sequence b for the row tile of query rows i0 .. i1;
+// slot: where its partial results go if they are not all (a team's range holds at
+// most one cut piece that ends in it, its first, and one that goes on, its last).
+__device__ __forceinline__ void latent_fill(const LatentArgs& a, LatentItem& d, int b, int kv_len, int t0, int t1,
+                                            bool whole, int slot, int i0, int i1) {
+  const int L = latent_len(a, kv_len);
+  int first, n;
+  latent_tiles(a, L, first, n);
+  d.b = b;
+  d.L = L;
+  d.first = first + t0;
+  d.n = n == 0 ? 0 : t1 - t0;
+  d.part = whole ? -1 : slot;
+  latent_visible(a, L, i0, d.lo_u, d.hi_x);
+  latent_visible(a, L, i1, d.lo_x, d.hi_u);
+}
+
 template <int R_, bool FP8_, int NT_>
 struct LatentCfg {
   static constexpr int R = R_, NT = NT_, NB = R / 128;
@@ -264,32 +401,8 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
   int* sums = reinterpret_cast<int*>(smem + C::OFF_MISC + 16);  // [WARPS]
   LatentItem* items = reinterpret_cast<LatentItem*>(smem + C::OFF_ITEM);
 
-  // The sequences' shares of the line (the loads go out first). Up to 128: the
-  // schedule warp has them to itself, four consecutive ones a lane; more: every
-  // warp adds up one chunk, and the schedule warp looks into the chunks it needs.
-  constexpr int K = 4;
-  const bool few = a.B <= 32 * K;
-  const int chunk = (a.B + C::WARPS - 1) / C::WARPS;
-  int w_sum = 0;  // (the host refuses calls of 2^31 tiles or more)
-  int lens[K], wts[K];
-#pragma unroll
-  for (int k = 0; k < K; ++k) lens[k] = wts[k] = 0;
-  auto share_of = [&](int L) {
-    if (blockIdx.x == 0 && (L < 0 || L > (a.max_pages << a.log2_page))) record_error_at(a.err, kErrBadPage);
-    return latent_weight(a, L);
-  };
-  if (!few) {
-    for (int b = warp * chunk + lane; b < min(a.B, (warp + 1) * chunk); b += 32) w_sum += share_of(__ldg(a.kv_lens + b));
-  } else if (warp == 3) {
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-      if (lane * K + k < a.B) lens[k] = __ldg(a.kv_lens + lane * K + k);
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      if (lane * K + k < a.B) wts[k] = share_of(lens[k]);
-      w_sum += wts[k];
-    }
-  }
+  LatentShares shares;  // (the loads go out first)
+  latent_load_shares<C::WARPS>(a, shares, warp, lane, warp == 3);
   if (tid < C::BARS) {
     uint64_t* bar = full + tid;
     const uint32_t count = bar >= p_ready && bar < o_full                 ? C::SOFT_THREADS
@@ -308,8 +421,8 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  if (!few) {
-    const int sum = __reduce_add_sync(FULL, w_sum);
+  if (!shares.few) {
+    const int sum = __reduce_add_sync(FULL, shares.sum);
     if (lane == 0) sums[warp] = sum;
   }
   tmem_fence_before();
@@ -320,57 +433,17 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
 
   if (warp == 3) {
     // ======================= schedule (whole warp) =============================
-    // The line's length and this team's range [s, e) of it (a line shorter than
-    // the number of teams leaves the last ones idle, so that no range is empty);
-    // then every sequence that overlaps the range becomes an item.
-    const int own_sum = few ? w_sum : lane < C::WARPS ? sums[lane] : 0;
-    int upto = own_sum;  // up to and with this lane's sequences, or chunk `lane`
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(FULL, upto, o);
-      if (lane >= o) upto += y;
-    }
-    const int total = __shfl_sync(FULL, upto, 31);
-    // the first `more` teams take share + 1 units, the rest share
-    const int teams = min(a.teams, total), share = total / teams, more = total - share * teams;
-    const int s = team < teams ? share * team + min(team, more) : total;
-    const int e = team < teams ? s + share + (team < more ? 1 : 0) : 0;
     const int i0 = rt * NT / a.H, i1 = (min(a.M, rt * NT + NT) - 1) / a.H;  // query rows of the row tile
     int j = 0;
     bool ok = true;
-    int cut_b = -1, cut_last = 0;  // the cut sequence that starts here and the unit of its last tile
-    auto publish = [&](int b, int kv_len, int begin, int w) {  // uniform over the warp
+    auto publish = [&](int b, int kv_len, int t0, int t1, bool whole, bool goes_on) {  // uniform over the warp
       if (j >= C::ITEMS)
         ok = __all_sync(FULL, wait_or_abort(&item_free[j % C::ITEMS], ((j / C::ITEMS) - 1) & 1, abort_flag, a.err));
       if (!ok) return;
       LatentItem& d = items[j % C::ITEMS];
-      if (b >= 0) {
-        const int L = latent_len(a, kv_len), t0 = max(s, begin) - begin, t1 = min(e, begin + w) - begin;
-        const bool whole = t0 == 0 && t1 == w;
-        int first, n;
-        latent_tiles(a, L, first, n);
-        int lo_u, hi_u, lo_x, hi_x;
-        latent_visible(a, L, i0, lo_u, hi_x);
-        latent_visible(a, L, i1, lo_x, hi_u);
-        if (lane == 0) {
-          d.b = b;
-          d.L = L;
-          d.first = first + t0;
-          d.n = n == 0 ? 0 : t1 - t0;
-          // a team's range holds at most one cut piece that ends in it (its
-          // first) and one that goes on behind it (its last)
-          d.part = whole ? -1 : (team * a.row_tiles + rt) * 2 + (begin + w > e ? 1 : 0);
-          d.lo_u = lo_u;
-          d.hi_u = hi_u;
-          d.lo_x = lo_x;
-          d.hi_x = hi_x;
-        }
-        if (t0 == 0 && !whole) {
-          cut_b = b;
-          cut_last = begin + w - 1;
-        }
-      } else if (lane == 0) {
-        d.b = -1;
+      if (lane == 0) {
+        if (b >= 0) latent_fill(a, d, b, kv_len, t0, t1, whole, (team * a.row_tiles + rt) * 2 + goes_on, i0, i1);
+        else d.b = -1;
       }
       __syncwarp();
       mbar_arrive(&item_full[j % C::ITEMS]);
@@ -386,55 +459,9 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
       }
       ++j;
     };
-    if (few) {
-      int begin[K], hits = 0;
-      begin[0] = upto - own_sum;
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        if (k > 0) begin[k] = begin[k - 1] + wts[k - 1];
-        if (wts[k] > 0 && begin[k] < e && begin[k] + wts[k] > s && s < e) hits |= 1 << k;
-      }
-      unsigned lanes = __ballot_sync(FULL, hits != 0);
-      while (lanes && ok) {
-        const int src = __ffs(lanes) - 1, mask = __shfl_sync(FULL, hits, src);
-        lanes &= lanes - 1;
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-          if (ok && (mask >> k & 1))
-            publish(src * K + k, __shfl_sync(FULL, lens[k], src), __shfl_sync(FULL, begin[k], src),
-                    __shfl_sync(FULL, wts[k], src));
-      }
-    }
-    // more: the chunk that holds unit s, then on to the range's end
-    int w = few ? -1 : __ffs(__ballot_sync(FULL, s < e && upto > s)) - 1;
-    int at = __shfl_sync(FULL, upto - own_sum, max(w, 0));  // where the sequences looked at next begin
-    for (; w >= 0 && w < C::WARPS && ok && at < e; ++w) {
-      const int b1 = min(a.B, (w + 1) * chunk);
-      for (int b0 = w * chunk; b0 < b1 && ok && at < e; b0 += 32) {
-        const int len = b0 + lane < b1 ? __ldg(a.kv_lens + b0 + lane) : 0;
-        const int wt = b0 + lane < b1 ? latent_weight(a, len) : 0;
-        int inc = wt;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(FULL, inc, o);
-          if (lane >= o) inc += y;
-        }
-        const int begin = at + inc - wt;
-        unsigned hit = __ballot_sync(FULL, wt > 0 && begin < e && begin + wt > s);
-        while (hit && ok) {
-          const int src = __ffs(hit) - 1;
-          hit &= hit - 1;
-          publish(b0 + src, __shfl_sync(FULL, len, src), __shfl_sync(FULL, begin, src), __shfl_sync(FULL, wt, src));
-        }
-        at += __shfl_sync(FULL, inc, 31);
-      }
-    }
-    if (ok) publish(-1, 0, 0, 0);
+    const int2 cut = latent_schedule<C::WARPS>(a, shares, sums, team, lane, ok, publish);
     if (!ok) *abort_flag = 1;
-    if (rt == 0 && lane == 0) {  // the team of the cut sequence's last tile
-      const int wide = (share + 1) * more;
-      a.cut[team] = make_int2(cut_b, cut_last < wide ? cut_last / (share + 1) : more + (cut_last - wide) / share);
-    }
+    if (rt == 0 && lane == 0) a.cut[team] = cut;
     __syncwarp();
   } else if (warp == 0) {
     // ======================= TMA producer (whole warp) =========================
