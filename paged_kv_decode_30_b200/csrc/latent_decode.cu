@@ -123,6 +123,7 @@ pda_status paged_latent_decode(const void* q, const void* latent_pages, const vo
   c.nt = pl.nt;
   c.row_tiles = pl.row_tiles;
   c.teams = pl.teams;
+  c.sms = sms;
   const cudaError_t e = fp8 ? launch_latent_decode_fp8(c, stream) : launch_latent_decode_bf16(c, stream);
   if (e == cudaErrorNotSupported) return PDA_ERR_UNSUPPORTED;
   return e == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;

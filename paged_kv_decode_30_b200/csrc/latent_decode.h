@@ -17,7 +17,7 @@ struct LatentCall {
   int* err;
   float *o_part, *lse_part;
   void* cut;
-  int nt, row_tiles, teams;
+  int nt, row_tiles, teams, sms;
 };
 
 cudaError_t launch_latent_decode_bf16(const LatentCall& c, cudaStream_t stream);

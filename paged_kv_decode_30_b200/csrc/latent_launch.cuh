@@ -62,7 +62,9 @@ cudaError_t launch_latent(const LatentCall& c, cudaStream_t stream) {
   e = cudaGetLastError();
   if (e != cudaSuccess || a.teams == 1) return e;  // one team cuts no sequence
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min(a.teams * a.row_tiles * 2, 2 * kMergeTeams));
+  // a block for each row of the sequences that can be cut, up to two an SM
+  const long long cut_rows = (long long)std::min(a.B, a.teams - 1) * a.M;
+  cfg.gridDim = dim3((unsigned)std::min(cut_rows, 2ll * c.sms));
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
