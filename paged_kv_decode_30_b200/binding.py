@@ -461,6 +461,12 @@ def _current_stream(device, stream):
     return torch._C._cuda_getCurrentRawStream(device.index) or None
 
 
+def _check_mask(causal_offset, window):
+    """Refuse what would not arrive: the library's fields have 32 bits."""
+    if not -0x80000000 <= min(causal_offset, window) <= max(causal_offset, window) <= 0x7FFFFFFF:
+        raise ValueError("causal_offset and window must fit 32 bits")
+
+
 def _used_on(stream, *tensors):
     """Tell the allocator that `stream` uses tensors made on the current one."""
     if stream is not None:
@@ -581,6 +587,7 @@ def paged_latent_decode(q, latent_pages, rope_pages, page_table, kv_lens, *, sca
     _, q_len, H, _ = _sizes("q", q, 4)
     _check("q", q, torch.bfloat16, (B, q_len, H, width + rope_dim), dev)
     _check("kv_lens", kv_lens, torch.int32, (B,), dev)
+    _check_mask(causal_offset, window)
     handle = _current_stream(dev, stream)
     if out is None:
         out = q.new_empty((B, q_len, H, width))
@@ -592,7 +599,10 @@ def paged_latent_decode(q, latent_pages, rope_pages, page_table, kv_lens, *, sca
         lse = q.new_empty((B, q_len, H), dtype=torch.float32)
     p = PdaLatentParams(B, q_len, H, width, rope_dim, page, max_pages, num_pages, scale,
                         causal_offset, window, kv_dtype, flags, _ptr(latent_scales), None, 0)
-    if workspace is None and not library_workspace:
+    if workspace is not None:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    elif not library_workspace:
         need = lib.paged_latent_decode_workspace_bytes(p)
         if need == ctypes.c_size_t(-1).value:
             need = 0  # the call below says what is wrong
@@ -630,6 +640,7 @@ def latent_prefill_attn(q, kv, k_rope, q_offsets, kv_offsets, *, scale,
     _check("k_rope", k_rope, torch.bfloat16, (total_kv, width - D), dev, rows=True)
     _check("q_offsets", q_offsets, torch.int32, (B + 1,), dev)
     _check("kv_offsets", kv_offsets, torch.int32, (B + 1,), dev)
+    _check_mask(causal_offset, window)
     handle = _current_stream(dev, stream)
     if out is None:
         out = q.new_empty((total_q, H, D))
@@ -639,7 +650,7 @@ def latent_prefill_attn(q, kv, k_rope, q_offsets, kv_offsets, *, scale,
         _check("lse", lse, torch.float32, (total_q, H), dev)
     elif with_lse:
         lse = q.new_empty((total_q, H), dtype=torch.float32)
-    p = PdaLatentPrefillParams(B, total_q, total_kv, total_q if max_q_len is None else max_q_len, H,
+    p = PdaLatentPrefillParams(B, total_q, total_kv, total_q if max_q_len is None else min(max_q_len, total_q), H,
                                D, width - D, _row_stride(k_rope), scale, causal_offset, window)
     st = lib.latent_prefill_attn(q.data_ptr(), kv.data_ptr(), k_rope.data_ptr(), q_offsets.data_ptr(),
                                  kv_offsets.data_ptr(), p, out.data_ptr(), _ptr(lse), handle)

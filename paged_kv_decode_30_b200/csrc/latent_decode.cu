@@ -27,7 +27,8 @@ pda_status validate(const pda_latent_params* p) {
   if (p->causal_offset < PDA_CAUSAL_BOTTOM_RIGHT) return PDA_ERR_INVALID_ARG;
   if (p->kv_dtype != PDA_KV_BF16 && p->kv_dtype != PDA_KV_FP8_E4M3 && p->kv_dtype != PDA_KV_NVFP4)
     return PDA_ERR_INVALID_ARG;
-  if ((long long)p->max_pages_per_seq * p->page_size > INT_MAX ||
+  // (a position and a tile more fit 32 bits)
+  if ((long long)p->max_pages_per_seq * p->page_size > INT_MAX - 128 ||
       (long long)p->num_pages * p->page_size > INT_MAX)
     return PDA_ERR_INVALID_ARG;
   if (p->flags & ~PDA_FLAG_NO_PDL) return PDA_ERR_INVALID_ARG;

@@ -51,7 +51,7 @@ extern "C" pda_status latent_prefill_attn(const void* q, const void* kv, const v
       !al(kv_offsets, 4) || !al(lse, 4))
     return PDA_ERR_MISALIGNED;
   const int rows = p.max_q_len < p.total_q ? p.max_q_len : p.total_q;
-  const long long tiles = (rows + 2 * PrefillCfg::QT - 1) / (2 * PrefillCfg::QT);
+  const long long tiles = (rows + 2ll * PrefillCfg::QT - 1) / (2 * PrefillCfg::QT);
   if (tiles * p.batch * p.num_heads > INT_MAX) return PDA_ERR_UNSUPPORTED;
   PrefillArgs a{};
   a.q_offsets = q_offsets;

@@ -167,6 +167,30 @@ def test_binding_refuses_host_tensors():
                               torch.zeros((5, 64), dtype=torch.bfloat16), off, off, scale=1.0)
 
 
+def test_lengths_near_32_bits(lib):
+    """A position and the tile behind it fit 32 bits, or the call is refused."""
+    over = dict(page_size=8, num_pages=9)
+    size = lambda n: lib.paged_latent_decode_workspace_bytes(ctypes.byref(
+        decode_params(batch=1, max_pages_per_seq=n, **over)))
+    assert size((2 ** 31 - 136) // 8) != ctypes.c_size_t(-1).value
+    assert size((2 ** 31 - 120) // 8) == ctypes.c_size_t(-1).value
+    assert decode(lib, decode_params(batch=1, max_pages_per_seq=(2 ** 31 - 120) // 8, **over)) == 1
+
+
+@pytest.mark.parametrize("over", [dict(window=1 << 31), dict(window=(1 << 32) + 5),
+                                  dict(causal_offset=1 << 31), dict(causal_offset=-(1 << 32) - 1)])
+def test_binding_refuses_masks_past_32_bits(over):
+    with pytest.raises(ValueError, match="32 bits"):
+        ch = L.cache([5], 8, 256, 32, False, 1)
+        B.paged_latent_decode(torch.zeros((1, 1, 4, 288), dtype=torch.bfloat16), ch["latent"], ch["rope"],
+                              ch["page_table"], ch["kv_lens"], scale=1.0, **over)
+    with pytest.raises(ValueError, match="32 bits"):
+        off = L.offsets([5])
+        B.latent_prefill_attn(torch.zeros((5, 2, 192), dtype=torch.bfloat16),
+                              torch.zeros((5, 2, 256), dtype=torch.bfloat16),
+                              torch.zeros((5, 64), dtype=torch.bfloat16), off, off, scale=1.0, **over)
+
+
 def test_quantiser_of_the_tests_at_its_borders():
     """The rule's borders by hand: 448 fits exponent 0, the next bf16 does not; zero and tiny
     rows take the least exponent, infinity the greatest."""

@@ -88,6 +88,18 @@ def test_append_bits(fp8, R, Dr, page, lens, before):
         assert (x is None and y is None) or torch.equal(bits(x), bits(y))
 
 
+@pytest.mark.parametrize("count", [31, 32, 1023, 1024, 1500])
+def test_append_many_sequences(count):
+    """Each way of finding a row's sequence, at its ends; a third of them get no rows."""
+    for most in (3, 6):   # few rows, and many
+        lens = [i % most for i in range(count)]
+        k = _append_case(lens, [(5 * i) % 11 for i in range(count)], 8, 256, 32, True, count)
+        got = _append_run(k)
+        clear()
+        for x, y in zip(got, _append_reference(k)):
+            assert torch.equal(bits(x), bits(y)), most
+
+
 def test_append_fp8_borders():
     """Rows at the borders of the exponent rule, infinities, NaN, zeros and ties."""
     R = 256
@@ -225,6 +237,9 @@ DECODE = [
     ([600, 64], 8, 20, 512, 64, 64, L.BOTTOM_RIGHT, 1),
     ([5000, 17, 1200], 1, 17, 512, 64, 64, L.OFF, 0),
     ([40] * 200, 1, 8, 512, 64, 16, L.OFF, 0),
+    ([i % 7 for i in range(1500)], 1, 4, 256, 32, 8, L.OFF, 0),
+    ([333, 70], 8, 256, 512, 64, 64, L.BOTTOM_RIGHT, 0),
+    ([1300, 0, 1], 5, 23, 256, 64, 8, L.BOTTOM_RIGHT, 500),
 ]
 
 
@@ -335,6 +350,77 @@ def test_decode_workspace_too_small():
         assert e.value.status == 4
 
 
+def test_decode_workspace_elsewhere():
+    ch, q, scale = _decode_inputs([1000, 70], 1, 32, 512, 64, 64, False, 6)
+    d = cuda(ch)
+    for ws in (torch.empty(64 << 20, dtype=torch.uint8),
+               torch.empty(64 << 20, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            _decode(d, q, scale, workspace=ws)
+
+
+def test_library_workspace_in_a_graph_is_refused():
+    ch, q, scale = _decode_inputs([1000, 70], 1, 32, 512, 64, 64, False, 6)
+    d, q = cuda(ch), q.cuda()
+    o, l = _decode(d, q, scale, library_workspace=True)   # grown already
+    x = torch.zeros(4, device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        with pytest.raises(B.PdaError) as e:
+            _decode(d, q, scale, out=o, lse=l, library_workspace=True)
+        x += 1
+    assert e.value.status == 4
+    g.replay()
+    torch.cuda.synchronize()
+    assert x.tolist() == [1.0] * 4
+    clear()
+
+
+def test_two_graphs_of_one_call_at_once():
+    """Two captures of the same call have workspaces of their own."""
+    ch, q, scale = _decode_inputs([1900, 5, 640, 3000], 1, 64, 512, 64, 64, False, 33)
+    d, q = cuda(ch), q.cuda()
+    want = _decode(d, q, scale)
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            graphs.append((g, torch.cuda.Stream(), _decode(d, q, scale)))
+    for _ in range(20):
+        for _, _, (o, l) in graphs:
+            o.zero_()
+            l.zero_()
+        torch.cuda.synchronize()
+        for g, s, _ in graphs:
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for _, _, (o, l) in graphs:
+            assert torch.equal(bits(o), bits(want[0])) and torch.equal(bits(l), bits(want[1]))
+    clear()
+
+
+def test_calls_with_nothing_to_do():
+    d = cuda(L.cache([20, 11], 8, 256, 32, False, 2))
+    none = d["page_table"][:0], d["kv_lens"][:0]
+    q = torch.zeros((0, 1, 4, 288), dtype=torch.bfloat16, device="cuda")
+    o, l = B.paged_latent_decode(q, d["latent"], d["rope"], *none, scale=1.0)
+    assert o.shape == (0, 1, 4, 256) and l.shape == (0, 1, 4)
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    c, r = B.paged_latent_gather(d["latent"], d["rope"], d["page_table"], off, total_rows=0)
+    assert c.shape == (0, 256) and r.shape == (0, 32)
+    before = d["latent"].clone(), d["rope"].clone()
+    B.paged_latent_append(c, r, off, d["page_table"], d["kv_lens"], d["latent"], d["rope"])
+    q = torch.zeros((0, 2, 192), dtype=torch.bfloat16, device="cuda")
+    kv = torch.zeros((7, 2, 256), dtype=torch.bfloat16, device="cuda")
+    o, l = B.latent_prefill_attn(q, kv, kv[:, 0, :64], off, off, scale=1.0)
+    assert o.shape == (0, 2, 128) and l.shape == (0, 2)
+    clear()
+    assert torch.equal(bits(before[0]), bits(d["latent"])) and torch.equal(bits(before[1]), bits(d["rope"]))
+
+
 def test_decode_reports_bad_places():
     for what in ("page", "long", "negative"):
         ch, q, scale = _decode_inputs([300, 50], 1, 16, 512, 64, 64, False, 8)
@@ -408,6 +494,9 @@ PREFILL = [
     ([260], [600], 1, 64, L.OFF, 33),
     ([1, 1, 1, 1], [1, 127, 128, 1025], 5, 64, L.BOTTOM_RIGHT, 0),
     ([700], [700], 1, 64, 650, 90),
+    ([5, 0, 300], [0, 0, 0], 2, 64, L.BOTTOM_RIGHT, 0),                  # no keys at all
+    ([1 + i % 7 for i in range(450)], [3 + i % 5 for i in range(450)], 2, 32, L.BOTTOM_RIGHT, 0),
+    ([300, 1] + [2] * 190, [310, 400] + [9] * 190, 1, 64, L.BOTTOM_RIGHT, 0),   # 384 pairs of sequence and tile
 ]
 
 
@@ -461,6 +550,20 @@ def test_prefill_rows_outside_and_strided_rope():
     L.check(out[3:3 + n], lse[3:3 + n], ref, 192, "outside")
     for t in (out, lse):
         assert bool((t[:3] == 7).all()) and bool((t[3 + n:] == 7).all())
+
+
+def test_prefill_computes_the_rows_of_max_q_len():
+    """Rows past max_q_len are not computed; rows behind it keep what they held."""
+    q_lens, kv_lens = [300, 20], [400, 20]
+    q, kv, r, scale = _prefill_inputs(q_lens, kv_lens, 2, 64, 8)
+    ref = L.prefill_reference(q, kv, r, q_lens, kv_lens, scale, L.BOTTOM_RIGHT, 0)
+    out = torch.full((320, 2, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    o, l = B.latent_prefill_attn(q.cuda(), kv.cuda(), r.cuda(), L.offsets(q_lens).cuda(),
+                                 L.offsets(kv_lens).cuda(), scale=scale, max_q_len=150, out=out)
+    clear()
+    for a, e in ((0, 150), (300, 320)):
+        L.check(o[a:e], l[a:e], (ref[0][a:e], ref[1][a:e], ref[2][a:e], ref[3]), 192, "bounded")
+    assert bool((o[150:300] == 7.0).all())
 
 
 def test_prefill_reports_bad_offsets():
