@@ -449,13 +449,15 @@ def _sizes(name, t, dims):
     return t.shape
 
 
-def _current_stream(device, stream):
+def _current_stream(device, stream=None):
     """The CUDA stream handle of a call on tensors of `device`: the given stream,
     or the current one. The library works on the current device, so tensors of
     another are refused."""
     if device.type != "cuda" or device.index != torch.cuda.current_device():
         raise ValueError(f"the tensors are on {device}, which is not the current CUDA device")
     if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
         return stream.cuda_stream or None
     # (the handle itself: the Stream object around it costs two microseconds)
     return torch._C._cuda_getCurrentRawStream(device.index) or None
@@ -467,12 +469,18 @@ def _check_mask(causal_offset, window):
         raise ValueError("causal_offset and window must fit 32 bits")
 
 
-def _used_on(stream, *tensors):
-    """Tell the allocator that `stream` uses tensors made on the current one."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+def _on(stream, call, *args, **kw):
+    """`call` with `stream` as the current stream, so that what it allocates is ordered
+    on that stream (a block that the caller's stream gave back may still be in use
+    there). The allocator learns that both streams use the results."""
+    caller = torch.cuda.current_stream(args[0].device)
+    with torch.cuda.stream(stream):
+        res = call(*args, **kw)
+    for t in (*res, kw.get("workspace")):
+        if t is not None:
+            t.record_stream(caller)
+            t.record_stream(stream)
+    return res
 
 
 def _row_stride(t):
@@ -553,6 +561,10 @@ def paged_latent_gather(latent_pages, rope_pages, page_table, row_offsets, *, to
     row_offsets[b + 1] of the outputs. Returns (latent [rows, R], rope [rows,
     Dr]): the given ones (rows behind row_offsets[B] are left alone), or new
     ones of total_rows rows."""
+    if stream is not None:
+        return _on(stream, paged_latent_gather, latent_pages, rope_pages, page_table, row_offsets,
+                   total_rows=total_rows, starts=starts, latent_scales=latent_scales, latent=latent,
+                   rope=rope)
     if latent is None or rope is None:
         if total_rows is None:
             raise ValueError("total_rows is needed to allocate the outputs")
@@ -565,10 +577,9 @@ def paged_latent_gather(latent_pages, rope_pages, page_table, row_offsets, *, to
     st = load().paged_latent_gather(latent_pages.data_ptr(), rope_pages.data_ptr(),
                                     page_table.data_ptr(), row_offsets.data_ptr(), _ptr(starts), p,
                                     latent.data_ptr(), rope.data_ptr(),
-                                    _current_stream(latent.device, stream))
+                                    _current_stream(latent.device))
     if st != 0:
         raise PdaError(st, "paged_latent_gather")
-    _used_on(stream, latent, rope)
     return latent, rope
 
 
@@ -581,6 +592,11 @@ def paged_latent_decode(q, latent_pages, rope_pages, page_table, kv_lens, *, sca
     the latents and its rotated part; out bf16 [B, q_len, H, R] is the weighted
     sum of latents, lse fp32 [B, q_len, H]. Pools as for paged_latent_append;
     masks and workspace as for paged_decode_attn."""
+    if stream is not None:
+        return _on(stream, paged_latent_decode, q, latent_pages, rope_pages, page_table, kv_lens,
+                   scale=scale, causal_offset=causal_offset, window=window,
+                   latent_scales=latent_scales, out=out, lse=lse, with_lse=with_lse,
+                   workspace=workspace, library_workspace=library_workspace, flags=flags)
     lib = load()
     dev, (num_pages, page, width), rope_dim, (B, max_pages), kv_dtype = _latent_pools(
         latent_pages, rope_pages, latent_scales, page_table)
@@ -588,7 +604,7 @@ def paged_latent_decode(q, latent_pages, rope_pages, page_table, kv_lens, *, sca
     _check("q", q, torch.bfloat16, (B, q_len, H, width + rope_dim), dev)
     _check("kv_lens", kv_lens, torch.int32, (B,), dev)
     _check_mask(causal_offset, window)
-    handle = _current_stream(dev, stream)
+    handle = _current_stream(dev)
     if out is None:
         out = q.new_empty((B, q_len, H, width))
     else:
@@ -616,7 +632,6 @@ def paged_latent_decode(q, latent_pages, rope_pages, page_table, kv_lens, *, sca
                                  _ptr(lse), handle)
     if st != 0:
         raise PdaError(st, "paged_latent_decode")
-    _used_on(stream, out, lse, workspace)
     return out, lse
 
 
@@ -629,6 +644,10 @@ def latent_prefill_attn(q, kv, k_rope, q_offsets, kv_offsets, *, scale,
     shared by the heads; q_offsets, kv_offsets int32 [B + 1]. ``max_q_len``:
     a bound on the query rows of a sequence (default total_q; a tighter one
     launches fewer idle CTAs). out bf16 [total_q, H, D], lse fp32 [total_q, H]."""
+    if stream is not None:
+        return _on(stream, latent_prefill_attn, q, kv, k_rope, q_offsets, kv_offsets, scale=scale,
+                   causal_offset=causal_offset, window=window, max_q_len=max_q_len, out=out,
+                   lse=lse, with_lse=with_lse)
     lib = load()
     dev = q.device
     total_q, H, width = _sizes("q", q, 3)
@@ -641,7 +660,7 @@ def latent_prefill_attn(q, kv, k_rope, q_offsets, kv_offsets, *, scale,
     _check("q_offsets", q_offsets, torch.int32, (B + 1,), dev)
     _check("kv_offsets", kv_offsets, torch.int32, (B + 1,), dev)
     _check_mask(causal_offset, window)
-    handle = _current_stream(dev, stream)
+    handle = _current_stream(dev)
     if out is None:
         out = q.new_empty((total_q, H, D))
     else:
@@ -656,7 +675,6 @@ def latent_prefill_attn(q, kv, k_rope, q_offsets, kv_offsets, *, scale,
                                  kv_offsets.data_ptr(), p, out.data_ptr(), _ptr(lse), handle)
     if st != 0:
         raise PdaError(st, "latent_prefill_attn")
-    _used_on(stream, out, lse)
     return out, lse
 
 

@@ -402,6 +402,35 @@ def test_two_graphs_of_one_call_at_once():
     clear()
 
 
+def test_outputs_of_another_stream():
+    """A call on a given stream gets no block that the caller's stream is still to
+    write: the results outlast the writes."""
+    ch, q, scale = _decode_inputs([1000, 70], 1, 32, 512, 64, 64, False, 6)
+    d, q = cuda(ch), q.cuda()
+    want = _decode(d, q, scale)
+    off = L.offsets([1000, 70]).cuda()
+    rows = B.paged_latent_gather(d["latent"], d["rope"], d["page_table"], off, total_rows=1070)
+    pq, kv, r, ps = (t.cuda() if torch.is_tensor(t) else t for t in _prefill_inputs([1000, 70], [1000, 70], 2, 64, 1))
+    wide = B.latent_prefill_attn(pq, kv, r, off, off, scale=ps)
+    s = torch.cuda.Stream()
+    calls = [(lambda: _decode(d, q, scale, stream=s), want),
+             (lambda: B.paged_latent_gather(d["latent"], d["rope"], d["page_table"], off, total_rows=1070, stream=s), rows),
+             (lambda: B.latent_prefill_attn(pq, kv, r, off, off, scale=ps, stream=s), wide)]
+    torch.cuda.synchronize()
+    for call, results in calls:
+        blocks = [torch.empty_like(t) for t in results]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)
+        for t in blocks:
+            t.fill_(float("nan"))
+        del blocks, t
+        got = call()
+        torch.cuda.synchronize()
+        for x, y in zip(got, results):
+            assert torch.equal(bits(x), bits(y))
+    clear()
+
+
 def test_calls_with_nothing_to_do():
     d = cuda(L.cache([20, 11], 8, 256, 32, False, 2))
     none = d["page_table"][:0], d["kv_lens"][:0]
