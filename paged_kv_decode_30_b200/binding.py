@@ -453,13 +453,14 @@ def _current_stream(device, stream=None):
     """The CUDA stream handle of a call on tensors of `device`: the given stream,
     or the current one. The library works on the current device, so tensors of
     another are refused."""
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
+    if device.type != "cuda" or device.index != torch._C._cuda_getDevice():
         raise ValueError(f"the tensors are on {device}, which is not the current CUDA device")
     if stream is not None:
         if stream.device != device:
             raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
         return stream.cuda_stream or None
-    # (the handle itself: the Stream object around it costs two microseconds)
+    # (the handle itself: the Stream object around it costs two microseconds; and a
+    # CUDA tensor is there, so that nothing is left to initialise)
     return torch._C._cuda_getCurrentRawStream(device.index) or None
 
 
@@ -522,18 +523,24 @@ def _latent_rows(latent, rope, row_offsets, page_table, starts, latent_pages, ro
     dev, (num_pages, page, width), rope_dim, (batch, max_pages), kv_dtype = _latent_pools(
         latent_pages, rope_pages, latent_scales, page_table)
     rows = _sizes("latent", latent, 2)[0]
+    c_strides = latent.stride()
     if not (latent.dtype is torch.bfloat16 and rope.dtype is torch.bfloat16
             and row_offsets.dtype is torch.int32 and latent.shape == (rows, width)
             and rope.shape == (rows, rope_dim) and row_offsets.shape == (batch + 1,)
             and latent.device == dev and rope.device == dev and row_offsets.device == dev
-            and latent.stride(1) == 1 and rope.stride(1) == 1 and row_offsets.is_contiguous()):
+            and c_strides[1] == 1 and (r_strides := rope.stride())[1] == 1
+            and row_offsets.is_contiguous()):
         _check("latent", latent, torch.bfloat16, (rows, width), dev, rows=True)
         _check("rope", rope, torch.bfloat16, (rows, rope_dim), dev, rows=True)
         _check("row_offsets", row_offsets, torch.int32, (batch + 1,), dev)
-    if starts is not None:
+    if starts is not None and not (starts.dtype is torch.int32 and starts.shape == (batch,)
+                                   and starts.device == dev and starts.is_contiguous()):
         _check("kv_lens / starts", starts, torch.int32, (batch,), dev)
+    if rows < 2:  # one row has no stride: its width, which any row count accepts
+        c_strides, r_strides = (width,), (rope_dim,)
     return PdaLatentRowsParams(batch, rows, width, rope_dim, page, max_pages, num_pages, kv_dtype,
-                               _row_stride(latent), _row_stride(rope), _ptr(latent_scales))
+                               c_strides[0], r_strides[0],
+                               None if latent_scales is None else latent_scales.data_ptr())
 
 
 def paged_latent_append(latent, rope, row_offsets, page_table, kv_lens, latent_pages, rope_pages,
@@ -601,8 +608,12 @@ def paged_latent_decode(q, latent_pages, rope_pages, page_table, kv_lens, *, sca
     dev, (num_pages, page, width), rope_dim, (B, max_pages), kv_dtype = _latent_pools(
         latent_pages, rope_pages, latent_scales, page_table)
     _, q_len, H, _ = _sizes("q", q, 4)
-    _check("q", q, torch.bfloat16, (B, q_len, H, width + rope_dim), dev)
-    _check("kv_lens", kv_lens, torch.int32, (B,), dev)
+    if not (q.dtype is torch.bfloat16 and kv_lens.dtype is torch.int32
+            and q.shape == (B, q_len, H, width + rope_dim) and kv_lens.shape == (B,)
+            and q.device == dev and kv_lens.device == dev
+            and q.is_contiguous() and kv_lens.is_contiguous()):
+        _check("q", q, torch.bfloat16, (B, q_len, H, width + rope_dim), dev)
+        _check("kv_lens", kv_lens, torch.int32, (B,), dev)
     _check_mask(causal_offset, window)
     handle = _current_stream(dev)
     if out is None:
