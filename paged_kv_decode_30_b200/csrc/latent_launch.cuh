@@ -41,7 +41,7 @@ cudaError_t launch_latent(const LatentCall& c, cudaStream_t stream) {
   a.row_tiles = c.row_tiles;
   a.scale_log2 = p.scale * 1.4426950408889634f;
   const long long rows = (long long)p.num_pages * p.page_size;
-  const int box = p.page_size < C::UT ? p.page_size : C::UT;
+  const int box = p.page_size < kTile ? p.page_size : kTile;
   alignas(64) CUtensorMap mc, mr, mq;
   if (!make_tokens_map(&mc, c.latent_pages, R, rows, FP8 ? 1 : 2, box, C::COLS_U) ||
       !make_rows_map(&mr, c.rope_pages, p.rope_dim, rows, p.rope_dim, 2, box) ||
