@@ -36,8 +36,8 @@ pda_status validate(const pda_latent_params* p) {
       p->page_size < 8 || p->page_size > 256 || (p->page_size & (p->page_size - 1)) ||
       p->kv_dtype == PDA_KV_NVFP4 || p->q_len > 8 || p->num_heads > 256 || p->batch > 65535)
     return PDA_ERR_UNSUPPORTED;
-  if (p->batch * (((long long)p->max_pages_per_seq * p->page_size + 127) / 128) > INT_MAX)
-    return PDA_ERR_UNSUPPORTED;  // tiles are counted in 32 bits
+  if (p->batch * (((long long)p->max_pages_per_seq * p->page_size + 127) / 128 + 16) > INT_MAX)
+    return PDA_ERR_UNSUPPORTED;  // tiles, and a few more a sequence, are counted in 32 bits
   return PDA_OK;
 }
 

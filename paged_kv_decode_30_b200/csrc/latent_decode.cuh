@@ -17,11 +17,11 @@
 // later ones from L2, and the matrix products and the shared memory they are
 // fed from become the bound.
 //
-// Schedule: the tiles of all sequences form one line, cut into equal ranges
-// for `teams` teams; the CTAs of a team take the same range for one row tile
-// each, at the same time, so that HBM sees each tile once. A sequence that
-// lies in one range is finished by its CTA; one that is cut leaves partial
-// results that a second kernel joins. The ranges follow from kv_lens by a scan
+// Schedule: the tiles of all sequences form one line, with a gap for what a change
+// of sequence takes, cut into equal ranges for `teams` teams; the CTAs of a team
+// take the same range for one row tile each, at the same time, so that HBM sees
+// each tile once. A sequence that lies in one range is finished by its CTA; one
+// that is cut leaves partial results that a second kernel joins. The ranges follow from kv_lens by a scan
 // that every CTA makes for itself: no counters, no atomics, one order of sums.
 //
 // FP8 rows are e4m3 codes with a power-of-two scale 2^e a row. Codes go to the
@@ -59,7 +59,7 @@ struct LatentArgs {
   float* lse_part;  // [teams * row_tiles * 2][NT]
   int2* cut;        // [teams]: (sequence, last team) of the cut sequence that starts in the team
   int B, Lq, H, M, rope_dim, page_size, log2_page, max_pages, num_pages, causal_offset, window;
-  int teams, row_tiles;
+  int teams, row_tiles, item_cost;
   float scale_log2;
 };
 
@@ -163,7 +163,10 @@ __device__ __forceinline__ int2 latent_schedule(const LatentArgs& a, const Laten
     const int y = __shfl_up_sync(FULL, upto, o);
     if (lane >= o) upto += y;
   }
-  const int total = __shfl_sync(FULL, upto, 31);
+  // A sequence after a range's first costs what item_cost tiles cost (less where a
+  // range is short): the line has gaps of that length between the sequences.
+  const int tiles = __shfl_sync(FULL, upto, 31);
+  const int gap = min(a.item_cost, max(tiles / a.teams - 1, 0)), total = tiles + gap * (a.B - 1);
   // the first `more` teams take share + 1 units, the rest share
   const int teams = min(a.teams, total), share = total / teams, more = total - share * teams;
   const int s = team < teams ? share * team + min(team, more) : total;
@@ -180,10 +183,10 @@ __device__ __forceinline__ int2 latent_schedule(const LatentArgs& a, const Laten
   };
   if (sh.few) {
     int begin[K], hits = 0;
-    begin[0] = upto - own_sum;
+    begin[0] = upto - own_sum + gap * lane * K;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if (k > 0) begin[k] = begin[k - 1] + sh.wts[k - 1];
+      if (k > 0) begin[k] = begin[k - 1] + sh.wts[k - 1] + gap;
       if (sh.wts[k] > 0 && begin[k] < e && begin[k] + sh.wts[k] > s && s < e) hits |= 1 << k;
     }
     unsigned lanes = __ballot_sync(FULL, hits != 0);
@@ -198,11 +201,12 @@ __device__ __forceinline__ int2 latent_schedule(const LatentArgs& a, const Laten
     }
   } else {
     // the chunk that holds unit s, then on to the range's end
-    int w = __ffs(__ballot_sync(FULL, s < e && upto > s)) - 1;
-    int at = __shfl_sync(FULL, upto - own_sum, max(w, 0));  // where the sequences looked at next begin
-    for (; w >= 0 && w < WARPS && ok && at < e; ++w) {
+    const int end = upto + gap * (min(a.B, (lane + 1) * sh.chunk) - 1);
+    int w = __ffs(__ballot_sync(FULL, s < e && end > s)) - 1;
+    int at = __shfl_sync(FULL, upto - own_sum, max(w, 0));  // tiles before the sequences looked at next
+    for (; w >= 0 && w < WARPS && ok && at + gap * (w * sh.chunk) < e; ++w) {
       const int b1 = min(a.B, (w + 1) * sh.chunk);
-      for (int b0 = w * sh.chunk; b0 < b1 && ok && at < e; b0 += 32) {
+      for (int b0 = w * sh.chunk; b0 < b1 && ok && at + gap * b0 < e; b0 += 32) {
         const int len = b0 + lane < b1 ? __ldg(a.kv_lens + b0 + lane) : 0;
         const int wt = b0 + lane < b1 ? latent_weight(a, len) : 0;
         int inc = wt;
@@ -211,7 +215,7 @@ __device__ __forceinline__ int2 latent_schedule(const LatentArgs& a, const Laten
           const int y = __shfl_up_sync(FULL, inc, o);
           if (lane >= o) inc += y;
         }
-        const int begin = at + inc - wt;
+        const int begin = at + inc - wt + gap * (b0 + lane);
         unsigned hit = __ballot_sync(FULL, wt > 0 && begin < e && begin + wt > s);
         while (hit && ok) {
           const int src = __ffs(hit) - 1;
@@ -319,6 +323,12 @@ struct LatentCfg {
   // largest weight. A smaller HEAD moves less often (72 sequences of up to 6000
   // tokens: 71.6 us at 0, 74.7 at 4, 77.0 at 6) but loses more of long flat tails.
   static constexpr float HEAD = FP8 ? 4.f : 0.f, TOP = FP8 ? 8.75f : 8.f;
+  // What a change of sequence takes, in tiles (queries, sums and stores; bf16 tiles
+  // are twice as long, and go on being loaded meanwhile). Us at 0 / 1 / 2 / 3 / 4 / 6:
+  // bf16, 32 rows, 300 sequences of up to 1500 tokens 69.8 / 65.4 / 67.8 / 70.7 / 72.3
+  // / 76.7; FP8, 16 rows, 200 of up to 4000 70.4 / 64.0 / 60.8 / 56.0 / 57.8 / 58.9; 48
+  // rows, 72 of up to 6000 70.0 / 66.7 / 62.0 / 58.6 / 55.8 / 57.0.
+  static constexpr int ITEM_COST = !FP8 ? 1 : NT == 16 ? 3 : 4;
 };
 
 __device__ __forceinline__ void l2_prefetch(const void* p, uint32_t bytes) {

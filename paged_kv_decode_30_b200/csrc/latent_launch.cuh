@@ -39,6 +39,7 @@ cudaError_t launch_latent(const LatentCall& c, cudaStream_t stream) {
   a.window = p.window;
   a.teams = c.teams;
   a.row_tiles = c.row_tiles;
+  a.item_cost = C::ITEM_COST;
   a.scale_log2 = p.scale * 1.4426950408889634f;
   const long long rows = (long long)p.num_pages * p.page_size;
   const int box = p.page_size < kTile ? p.page_size : kTile;
