@@ -1036,7 +1036,11 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
 // lse = ln sum_k exp(lse_k), out = sum_k exp(lse_k - lse) o_k. Of a sequence of
 // few parts (most cuts leave two or three) a warp takes a row; of one of many
 // parts a block takes a row, WARPS / V warps with every so manyth part each.
-// Bound by latency: the list of cuts, then a row's lse and parts, loaded together.
+// Bound by latency: the list of cuts, then a row's lse and parts, loaded together;
+// and by the instructions themselves, which no SM has at hand when the main kernel
+// ends. A variant for 2, 3 and 4 parts each, loads of eight parts unrolled and the
+// exact exp2f took 3.4 us more (2 sequences of 110 k tokens, 64 heads: 54.8 us
+// instead of 51.4), more variants for 5 to 8 parts another 1.5 to 3.
 constexpr int kMergeFew = 4, kMergeTeams = 256, kMergeThreads = 512;
 
 template <int R>
@@ -1082,13 +1086,15 @@ __global__ void __launch_bounds__(kMergeThreads, 2) latent_merge_kernel(const La
   // sum_k exp(lse_k - m) and the largest lse_k, m; l0: this lane's
   auto row_lse = [&](const int3& c, int row, float l0, float& m) {
     m = l0;
+#pragma unroll 1
     for (int k = lane + 32; k < c.y; k += 32) m = fmaxf(m, a.lse_part[slot_of(c, row, k)]);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
     float sum = 0.f;
     if (m != -INFINITY) {
-      sum = exp2f((l0 - m) * kLog2e);
-      for (int k = lane + 32; k < c.y; k += 32) sum += exp2f((a.lse_part[slot_of(c, row, k)] - m) * kLog2e);
+      sum = fast_exp2((l0 - m) * kLog2e);
+#pragma unroll 1
+      for (int k = lane + 32; k < c.y; k += 32) sum += fast_exp2((a.lse_part[slot_of(c, row, k)] - m) * kLog2e);
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
@@ -1098,16 +1104,16 @@ __global__ void __launch_bounds__(kMergeThreads, 2) latent_merge_kernel(const La
     *reinterpret_cast<uint2*>(a.out + o * R + col) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
   };
 
-  // A row of P parts: all its loads go out together (of more than two parts in
-  // two halves of the columns, for the registers).
-  auto few_row = [&](auto parts, const int3& c, int row) {
-    constexpr int P = decltype(parts)::value, X = P <= 2 ? V : V / 2;
+  // A row of up to kMergeFew parts: all its loads go out together, in two halves
+  // of the columns for the registers.
+  auto few_row = [&](const int3& c, int row) {
+    constexpr int P = kMergeFew, X = V / 2;
     float l[P], m = -INFINITY;
     const float4* src[P];
 #pragma unroll
     for (int k = 0; k < P; ++k) {
-      const long long s = slot_of(c, row, k);
-      l[k] = a.lse_part[s];
+      const long long s = slot_of(c, row, min(k, c.y - 1));
+      l[k] = k < c.y ? a.lse_part[s] : -INFINITY;
       src[k] = reinterpret_cast<const float4*>(a.o_part + s * R) + lane;
     }
     const long long o = (long long)c.z * a.M + row;
@@ -1117,7 +1123,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) latent_merge_kernel(const La
 #pragma unroll
       for (int x = 0; x < X; ++x)
 #pragma unroll
-        for (int k = 0; k < P; ++k) q[x][k] = src[k][32 * (x0 + x)];
+        for (int k = 0; k < P; ++k) q[x][k] = k < 2 || k < c.y ? src[k][32 * (x0 + x)] : make_float4(0.f, 0.f, 0.f, 0.f);
       if (x0 == 0) {  // the parts' weights, and the row's lse
 #pragma unroll
         for (int k = 0; k < P; ++k) m = fmaxf(m, l[k]);
@@ -1147,9 +1153,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) latent_merge_kernel(const La
   for (int u = blockIdx.x * WARPS + warp; u < n_few * a.M; u += gridDim.x * WARPS) {
     const int ci = u / a.M, row = u - ci * a.M;
     const int3 c = cuts[ci];
-    if (c.y == 2) few_row(std::integral_constant<int, 2>{}, c, row);
-    else if (c.y == 3) few_row(std::integral_constant<int, 3>{}, c, row);
-    else few_row(std::integral_constant<int, 4>{}, c, row);
+    few_row(c, row);
   }
 
   for (int u = blockIdx.x; u < n_many * a.M; u += gridDim.x) {
@@ -1161,10 +1165,11 @@ __global__ void __launch_bounds__(kMergeThreads, 2) latent_merge_kernel(const La
     const float sum = row_lse(c, row, l0, m);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (m != -INFINITY) {
-#pragma unroll 8
+      const float inv = 1.f / sum;
+#pragma unroll 2
       for (int k = grp; k < c.y; k += GROUPS) {
         const long long s = slot_of(c, row, k);
-        const float w = exp2f((a.lse_part[s] - m) * kLog2e) / sum;  // 0 for a part without keys
+        const float w = fast_exp2((a.lse_part[s] - m) * kLog2e) * inv;  // 0 for a part without keys
         const float4 q = *(reinterpret_cast<const float4*>(a.o_part + s * R) + lane + 32 * x);
         acc.x = fmaf(w, q.x, acc.x);
         acc.y = fmaf(w, q.y, acc.y);
