@@ -37,8 +37,6 @@
 // Every wait is bounded.
 #pragma once
 
-#include <type_traits>
-
 #include "pda_device.cuh"
 #include "split_tma.cuh"  // MMA issue, instruction descriptors, TMA loads, e4m3 splits
 #include "tcgen05.cuh"
