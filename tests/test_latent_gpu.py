@@ -240,6 +240,10 @@ DECODE = [
     ([i % 7 for i in range(1500)], 1, 4, 256, 32, 8, L.OFF, 0),
     ([333, 70], 8, 256, 512, 64, 64, L.BOTTOM_RIGHT, 0),
     ([1300, 0, 1], 5, 23, 256, 64, 8, L.BOTTOM_RIGHT, 500),
+    # several sequences a team: with up to 128 of them, more, and two CTAs a team
+    ([(i * 397) % 1500 for i in range(100)], 1, 4, 256, 32, 32, L.OFF, 0),
+    ([(i * 211) % 900 for i in range(180)], 2, 3, 256, 64, 64, L.BOTTOM_RIGHT, 0),
+    ([(i * 397) % 1500 for i in range(60)], 1, 40, 512, 64, 64, L.OFF, 0),
 ]
 
 
