@@ -479,8 +479,10 @@ typedef struct {
  *              value up-projection).
  * lse          device, fp32 [B, q_len, H], natural log; may be NULL.
  * Accumulation and softmax statistics are fp32; each weight enters the sum
- * over values with 8 significant bits (FP8 caches: or to 2^-18 of the row's
- * largest weight, whichever is coarser).
+ * over values with 8 significant bits. FP8 caches: the weights are p_j = exp(s_j
+ * - lse) times their row's scale 2^e_j, and what is rounded off small ones beyond
+ * that adds up to at most 2^-8.9 of the row's sum of p_j 2^e_j, however many
+ * there are; a query element enters to 2^-21 of its row's largest.
  *
  * Slots of a page past kv_lens[b] and keys no row may see are never weighted
  * (their bytes may be NaN). q, pools and out 16-byte aligned, the rest 4-byte

@@ -28,8 +28,24 @@
 // matrix instructions as they are (kind::f8f6f4); a bf16 query row times a
 // power of two is the exact sum of two e4m3 terms [hi; 16 lo]; the rotated
 // parts are bf16 products into columns of their own. With x_j the score
-// (log2 units) the weight is w_j = 2^(x_j + e_j - m), m a running maximum of
+// (log2 units) the weight is w_j = 2^(x_j + e_j - m), m a reference that follows
 // x + e, split in two e4m3 terms as well; the normaliser adds w_j 2^-e_j.
+//
+// Two e4m3 terms hold a weight to 2^-8 of itself or to 2^-14, whichever is coarser.
+// A long flat tail below a peak can consist of weights under that step (131 k tokens
+// that share a fifth of the probability, the rest on one: all of them became zero,
+// a fifth of the output), so m follows the scores down as well as up. Per row a
+// credit counts how many tiles' worth of such errors, 128 x 2^-14 = 2^-7 each, the
+// weights have paid for: a tile takes one away, and one with a weight of 2, 8, 32 or 128
+// adds 1/2, 2, 8 or 32, a fourth of it. Before it is used up m moves to the tile at hand.
+// What the step rounds off is then at most 2^-7 / 4 = 2^-9 of a row's sum of weights
+// (2^-8.9, as the weights are compared rounded), whatever its length, and a row moves only
+// where its weights stay low. (Normally distributed scores, 2.5 in log2 units, rows of
+// different scales: a group of eight rows moves in 29% of 40 tiles instead of 12% with a
+// running maximum, in 22% of 400 instead of 2%; 2 in log2 units: 5% instead of 2%.)
+// Such scores take 57.3 us instead of 51.6 for two sequences of 110 k tokens, 64 heads,
+// and 61.6 instead of 57.1 for 72 of up to 6000 tokens, 48 rows; with 1/4 replaced by 1/2,
+// 55.3 and 60.4; with HEAD 4 or 6 instead of 5, 63.4 or 57.9 and 68.5 or 62.6.
 //
 // Roles (warps): 0 TMA producer, 1 S^T issuer, 2 O^T issuer, 3 schedule,
 // 4.. softmax (groups of four warps, a thread = a token of S^T = an element of
@@ -281,7 +297,7 @@ struct LatentCfg {
   static constexpr int P_BUFS = (OVERLAY || (NT == 32 && R == 512)) ? 1 : 2;
   static constexpr int R_SLOTS = FP8 && !(NT == 32 && R == 512) ? 2 : 1;
   static constexpr int ROPE_SLOT = HALF;
-  static constexpr int STATE = 20 * NT * 4 + 1024;
+  static constexpr int STATE = 20 * NT * 4 + 1024 + (FP8 ? NT * 4 : 0);
   static constexpr int FREE = 227 * 1024 - 1024 - STATE - Q_BYTES - (OVERLAY ? 0 : P_BUFS * P_BYTES) -
                               R_SLOTS * ROPE_SLOT;
   static constexpr int SLOTS = FREE / BLK < 3 * UPT ? FREE / BLK : 3 * UPT;
@@ -297,7 +313,9 @@ struct LatentCfg {
   static constexpr int OFF_INV = OFF_LRED + 8 * NT * 4;
   static constexpr int OFF_CS = OFF_INV + NT * 4;       // score scale per row (FP8)
   static constexpr int OFF_RANGE = OFF_CS + NT * 4;     // int2 visible keys per row
-  static constexpr int OFF_ITEM = OFF_RANGE + NT * 8;
+  static constexpr int OFF_LEVEL = OFF_RANGE + NT * 8;  // FP8: [2][4][NT / 8] levels of a tile's weights
+  static constexpr int OFF_CREDIT = OFF_LEVEL + (FP8 ? NT * 4 : 0);    // FP8: [NT] credit, [NT] greatest m
+  static constexpr int OFF_ITEM = OFF_CREDIT + (FP8 ? 2 * NT * 4 : 0);
   static constexpr int ITEMS = 4;
   static constexpr int OFF_BAR = OFF_ITEM + ITEMS * (int)sizeof(LatentItem);
   static constexpr int BARS = 2 * SLOTS + 2 * R_SLOTS + 2 + 2 + 2 + 3 + 2 * ITEMS;
@@ -315,12 +333,13 @@ struct LatentCfg {
   static constexpr int TMEM_COLS = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
   static_assert(COLS <= 512 && SLOTS >= UPT && SMEM_ALLOC <= 227 * 1024, "capacity");
   static_assert(BLK % 1024 == 0 && Q_BLK % 1024 == 0 && Q_BYTES % 1024 == 0 && P_BYTES % 1024 == 0, "alignment");
-  // A row's weights start at 2^HEAD for its largest score so far, and its maximum
-  // moves once one would pass 2^TOP (e4m3 holds 448 = 2^8.8). FP8: what the second
-  // term cannot hold, half its smallest step 2^-13, is then at most 2^-18 of the
-  // largest weight. A smaller HEAD moves less often (72 sequences of up to 6000
-  // tokens: 71.6 us at 0, 74.7 at 4, 77.0 at 6) but loses more of long flat tails.
-  static constexpr float HEAD = FP8 ? 4.f : 0.f, TOP = FP8 ? 8.75f : 8.f;
+  // A row's weights start at 2^HEAD for its largest score so far (exactly, so that a
+  // peak is not rounded: with m in whole numbers it was off by up to 2^-8), and m moves
+  // once one would pass 2^TOP (e4m3 holds 448 = 2^8.8). FP8: m moves down as well, by no
+  // more than DOWN below its greatest value: what rounds off there is 2^-50 of the
+  // largest weight a tile, and sums of 2^31 tokens, 2^30 the largest 2^-e, stay below
+  // 2^127.
+  static constexpr float HEAD = FP8 ? 5.f : 0.f, TOP = FP8 ? 8.75f : 8.f, DOWN = 40.f;
   // What a change of sequence takes, in tiles (queries, sums and stores; bf16 tiles
   // are twice as long, and go on being loaded meanwhile). Us at 0 / 1 / 2 / 3 / 4 / 6:
   // bf16, 32 rows, 300 sequences of up to 1500 tokens 69.8 / 65.4 / 67.8 / 70.7 / 72.3
@@ -342,6 +361,13 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       "[%0], [%1, {%2, %2, %3, %4}], [%5];" ::"r"(dst),
       "l"(map), "r"(0), "r"(col), "r"(group), "r"(smem_addr(bar))
       : "memory");
+}
+
+// Four e4m3 values >= 0 in a word: bits 6, 5, 4, 3 of each byte say whether its value
+// is at least 2, 8, 32, 128 (the exponent field, biased by 7, lies in bits 6 to 3).
+__device__ __forceinline__ uint32_t e4m3_levels(uint32_t v) {
+  const uint32_t l2 = v & 0x40404040u, b5 = v << 1, b4 = v << 2;
+  return l2 | (l2 & (b5 | b4)) >> 1 | (l2 & b5) >> 2 | (l2 & b5 & b4) >> 3;
 }
 
 // 128-byte-swizzled address of 16-byte piece c of row n in a block of rows.
@@ -691,6 +717,8 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
     float* lred = reinterpret_cast<float*>(smem + C::OFF_LRED);
     float* sm_inv = reinterpret_cast<float*>(smem + C::OFF_INV);
     float* sm_cs = reinterpret_cast<float*>(smem + C::OFF_CS);
+    uint32_t* sm_level = reinterpret_cast<uint32_t*>(smem + C::OFF_LEVEL) + grp;
+    float* sm_credit = reinterpret_cast<float*>(smem + C::OFF_CREDIT);
     int2* sm_range = reinterpret_cast<int2*>(smem + C::OFF_RANGE);
     const uint32_t s_tm = tmem + lane_off + C::COL_S + (FP8 ? 2 * r0 : r0);
     const uint32_t o_tm = tmem + lane_off + C::COL_O + (FP8 ? 2 * r0 : r0);
@@ -767,6 +795,10 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
         if (R0 + i < a.M) latent_visible(a, L, (R0 + i) / a.H, lo, hi);
         sm_range[r0 + i] = make_int2(lo, hi);
         sm_nm[r0 + i] = -kUnset;
+        if constexpr (FP8) {
+          sm_credit[r0 + i] = 2.f;  // (until the row's first key)
+          sm_credit[NT + r0 + i] = kUnset;
+        }
       }
       named_bar(gbar, GT);
       // FP8: this token's scale exponent, looked up a tile ahead
@@ -779,6 +811,7 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
         return __ldg(a.scales + (long long)page * a.page_size + (jt & (a.page_size - 1)));
       };
       int sc_next = scale_of(first);
+      bool low = false;  // FP8, threads i < rows: row i's credit runs out
       float l_sum[RH], l_rnd[RH];  // this token's part of the row sums: of the weights, of the rounded ones
 #pragma unroll
       for (int r = 0; r < RH; ++r) l_sum[r] = l_rnd[r] = 0.f;
@@ -863,7 +896,17 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
         float top = x[0];
 #pragma unroll
         for (int r = 1; r < RH; ++r) top = fmaxf(top, x[r]);
-        if (named_bar_or(gbar, GT, !good || top > C::TOP)) {
+        const bool moves = named_bar_or(gbar, GT, !good || top > C::TOP || low);
+        // FP8: a row's credit with the tile before, whose levels all warps have left by
+        // then. It is looked at a tile later still, so that two tiles have to be left.
+        auto credit_of = [&]() {
+          const uint32_t* lv = sm_level + ((g - 1) & 1) * 4 * C::GROUPS;
+          const uint32_t all = lv[0] | lv[C::GROUPS] | lv[2 * C::GROUPS] | lv[3 * C::GROUPS];
+          const int k = __popc((all >> (8 * (i & 3) + (i < 4 ? 4 : 0))) & 15u);
+          const float paid = k > 0 ? 0.5f * (float)(1 << (2 * k - 2)) : 0.f;
+          return sm_credit[r0 + i] + (t > first ? paid - 1.f : 0.f);
+        };
+        if (moves) {
           if (!named_bar_and(gbar, GT, good)) {
             ok = false;
             break;
@@ -878,9 +921,31 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
           if (i < RH) {
             const int rr = r0 + i;
             const float most = fmaxf(fmaxf(wmax[rr], wmax[NT + rr]), fmaxf(wmax[2 * NT + rr], wmax[3 * NT + rr]));
-            const float m_old = -sm_nm[rr], m_new = fmaxf(m_old, most - C::HEAD);
-            sm_alpha[rr] = fast_exp2(m_old - m_new);
-            sm_nm[rr] = -m_new;
+            const float m_old = -sm_nm[rr];
+            if constexpr (FP8) {
+              float m_new = most - C::HEAD;  // (-inf: no key of this tile is seen)
+              float credit = credit_of();
+              if (m_new > m_old) {
+                low = false;  // (the tile pays for itself and seven more)
+              } else if (low && most != -INFINITY) {
+                const float least = sm_credit[NT + rr] - C::DOWN;
+                if (m_new <= least) credit = 1e9f;  // the end of the way down: no more to pay
+                m_new = fminf(fmaxf(m_new, least), m_old);
+                low = false;
+              } else {
+                m_new = m_old;
+                low = i < rows && credit < 2.f;
+              }
+              const float al = fast_exp2(m_old - m_new);
+              sm_alpha[rr] = al;
+              sm_credit[rr] = credit * al;
+              sm_credit[NT + rr] = fmaxf(sm_credit[NT + rr], m_new);
+              sm_nm[rr] = -m_new;
+            } else {
+              const float m_new = fmaxf(m_old, most - C::HEAD);
+              sm_alpha[rr] = fast_exp2(m_old - m_new);
+              sm_nm[rr] = -m_new;
+            }
           }
           named_bar(gbar, GT);
           float al[RH];
@@ -946,6 +1011,15 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
           f2_unpack(FP8 ? f2_fma(v, f2_pack(down, down), old) : f2_add(v, old), l_sum[r], l_sum[r + 1]);
           if constexpr (!FP8)
             f2_unpack(f2_add(bf16x2_to_f2(w[r / 2]), f2_pack(l_rnd[r], l_rnd[r + 1])), l_rnd[r], l_rnd[r + 1]);
+        }
+        if constexpr (FP8) {  // which rows have a weight of 2, 8, 32, 128 in this tile
+          const uint32_t lv = __reduce_or_sync(FULL, e4m3_levels(w[0]) << 1 | e4m3_levels(w[1]) >> 3);
+          if (lane == 0) sm_level[((g & 1) * 4 + q4) * C::GROUPS] = lv;
+          if (!moves && i < rows) {
+            const float credit = credit_of();
+            sm_credit[r0 + i] = credit;
+            low = credit < 2.f;
+          }
         }
       }
       if (!ok) break;
