@@ -1040,11 +1040,12 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
         const float l = lred[rr] + lred[NT + rr] + lred[2 * NT + rr] + lred[3 * NT + rr];
         const float ln = FP8 ? l : lred[4 * NT + rr] + lred[5 * NT + rr] + lred[6 * NT + rr] + lred[7 * NT + rr];
         if (i < rows) {
-          const float lse = l > 0.f ? (log2f(l) - sm_nm[rr]) * kLn2 : -INFINITY;
+          // (0 without keys; NaN of a score that is NaN or +inf passes on)
+          const float lse = l == 0.f ? -INFINITY : (log2f(l) - sm_nm[rr]) * kLn2;
           if (part >= 0) a.lse_part[(long long)part * NT + rr] = lse;
           else if (a.lse) a.lse[(long long)b * a.M + R0 + i] = lse;
         }
-        sm_inv[rr] = ln > 0.f ? 1.f / ln : 0.f;
+        sm_inv[rr] = ln == 0.f ? 0.f : 1.f / ln;
       }
       named_bar(gbar, GT);
       float inv[RH];
@@ -1072,7 +1073,7 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
             tmem_ldn(o_tm + k * C::N2, o);
           }
 #pragma unroll
-          for (int r = 0; r < RH; ++r) o[r] = inv[r] > 0.f ? o[r] * inv[r] : 0.f;
+          for (int r = 0; r < RH; ++r) o[r] = inv[r] == 0.f ? 0.f : o[r] * inv[r];
         }
         if (part >= 0) {
 #pragma unroll
@@ -1105,7 +1106,8 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
 }
 
 // Joins the partial results of the sequences that lie in several teams' ranges:
-// lse = ln sum_k exp(lse_k), out = sum_k exp(lse_k - lse) o_k. Of a sequence of
+// lse = ln sum_k exp(lse_k), out = sum_k exp(lse_k - lse) o_k; a part whose lse is NaN
+// makes the row NaN. Of a sequence of
 // few parts (most cuts leave two or three) a warp takes a row; of one of many
 // parts a block takes a row, WARPS / V warps with every so manyth part each.
 // Bound by latency: the list of cuts, then a row's lse and parts, loaded together;
@@ -1155,19 +1157,17 @@ __global__ void __launch_bounds__(kMergeThreads, 2) latent_merge_kernel(const La
     return ((long long)(((c.x + k) * a.row_tiles + (row >> log2_nt)) * 2 + (k + 1 < c.y ? 1 : 0)) << log2_nt) +
            (row & ((1 << log2_nt) - 1));
   };
-  // sum_k exp(lse_k - m) and the largest lse_k, m; l0: this lane's
+  // sum_k exp(lse_k - m) and the largest lse_k (0 if all are -inf), m; l0: this lane's
   auto row_lse = [&](const int3& c, int row, float l0, float& m) {
     m = l0;
 #pragma unroll 1
     for (int k = lane + 32; k < c.y; k += 32) m = fmaxf(m, a.lse_part[slot_of(c, row, k)]);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
-    float sum = 0.f;
-    if (m != -INFINITY) {
-      sum = fast_exp2((l0 - m) * kLog2e);
+    if (m == -INFINITY) m = 0.f;
+    float sum = fast_exp2((l0 - m) * kLog2e);
 #pragma unroll 1
-      for (int k = lane + 32; k < c.y; k += 32) sum += fast_exp2((a.lse_part[slot_of(c, row, k)] - m) * kLog2e);
-    }
+    for (int k = lane + 32; k < c.y; k += 32) sum += fast_exp2((a.lse_part[slot_of(c, row, k)] - m) * kLog2e);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
     return sum;
@@ -1203,10 +1203,10 @@ __global__ void __launch_bounds__(kMergeThreads, 2) latent_merge_kernel(const La
         float sum = 0.f;
 #pragma unroll
         for (int k = 0; k < P; ++k) sum += l[k] = fast_exp2((l[k] - base) * kLog2e);
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
         for (int k = 0; k < P; ++k) l[k] *= inv;
-        if (lane == 0 && a.lse) a.lse[o] = m == -INFINITY ? -INFINITY : m + log2f(sum) * kLn2;
+        if (lane == 0 && a.lse) a.lse[o] = sum == 0.f ? -INFINITY : base + log2f(sum) * kLn2;
       }
 #pragma unroll
       for (int x = 0; x < X; ++x) {
@@ -1236,7 +1236,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) latent_merge_kernel(const La
     float m;
     const float sum = row_lse(c, row, l0, m);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (m != -INFINITY) {
+    if (sum != 0.f) {
       const float inv = 1.f / sum;
 #pragma unroll 2
       for (int k = grp; k < c.y; k += GROUPS) {
@@ -1262,7 +1262,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) latent_merge_kernel(const La
       }
       const long long o = (long long)c.z * a.M + row;
       store(o, (lane + 32 * x) * 4, acc);
-      if (x == 0 && lane == 0 && a.lse) a.lse[o] = m == -INFINITY ? -INFINITY : m + log2f(sum) * kLn2;
+      if (x == 0 && lane == 0 && a.lse) a.lse[o] = sum == 0.f ? -INFINITY : m + log2f(sum) * kLn2;
     }
     __syncthreads();
   }
