@@ -482,7 +482,8 @@ typedef struct {
  * over values with 8 significant bits. FP8 caches: the weights are p_j = exp(s_j
  * - lse) times their row's scale 2^e_j, and what is rounded off small ones beyond
  * that adds up to at most 2^-8.9 of the row's sum of p_j 2^e_j, however many
- * there are; a query element enters to 2^-21 of its row's largest.
+ * there are; a query element enters to 2^-21 of its row's largest, and
+ * an infinite one makes its row NaN.
  *
  * Slots of a page past kv_lens[b] and keys no row may see are never weighted
  * (their bytes may be NaN). q, pools and out 16-byte aligned, the rest 4-byte

@@ -766,7 +766,9 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
           // 2^e2 from the exponent field of mx (0 for a row of zeros; within 2^+-120)
           const int e2 = mx > 0.f ? min(max(134 - (int)(__float_as_uint(mx) >> 23), -120), 120) : 0;
           const float up = __int_as_float((127 + e2) << 23);
-          if (lane == 0) sm_cs[nrow] = a.scale_log2 * __int_as_float((127 - e2) << 23);
+          // (an infinite element, which e4m3 does not have, makes the row's scores NaN)
+          if (lane == 0)
+            sm_cs[nrow] = mx < INFINITY ? a.scale_log2 * __int_as_float((127 - e2) << 23) : __int_as_float(0x7FC00000);
           uint32_t hw[E / 4], lw[E / 4];
 #pragma unroll
           for (int x = 0; x < E / 4; ++x) {  // (bf16's 8 bits times 2^e2 fit f16, in which the split works)

@@ -50,7 +50,7 @@ def test_decode_of_a_key_that_is_not_finite(name, fp8, where):
     others(o, l, ref, rows, where, _fp8_of(ch) if fp8 else None)
 
 
-@pytest.mark.parametrize("fp8,value", [(False, NAN), (False, INF), (True, NAN)])
+@pytest.mark.parametrize("fp8,value", [(False, NAN), (False, INF), (True, NAN), (True, INF)])
 @pytest.mark.parametrize("name", RANGES)
 def test_decode_of_a_query_that_is_not_finite(name, fp8, value):
     """The row of that query is NaN (with an infinite element some keys' scores are +inf),
