@@ -508,7 +508,8 @@ __global__ void __launch_bounds__(PrefillCfg::THREADS, 1)
     ok = __all_sync(FULL, ok);
     if (ok) {
       tmem_fence_after();
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      // (the sum is 0 without keys; NaN of a score that is NaN or +inf passes on)
+      const float inv = l == 0.f ? 0.f : 1.f / l;
       const long long row = (long long)(qb + i) * a.H + h;
 #pragma unroll 2
       for (int c = 0; c < 4; ++c) {
@@ -521,13 +522,13 @@ __global__ void __launch_bounds__(PrefillCfg::THREADS, 1)
           uint32_t w[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k)
-            w[k] = inv > 0.f ? pack_bf16x2(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv) : 0u;
+            w[k] = inv == 0.f ? 0u : pack_bf16x2(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
           uint4* dst = reinterpret_cast<uint4*>(a.out + row * C::D + 32 * c);
 #pragma unroll
           for (int k = 0; k < 4; ++k) dst[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
         }
       }
-      if (live && a.lse) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+      if (live && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     } else {
       *abort_flag = 1;
     }

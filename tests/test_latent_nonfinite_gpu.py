@@ -79,3 +79,32 @@ def test_decode_of_a_query_that_sees_nothing_and_is_not_finite(fp8):
     o, l = _decode(cuda(ch), q, scale, causal_offset=L.BOTTOM_RIGHT)
     clear()
     L.check(o, l, ref, 576, "no keys", _fp8_of(ch))
+
+
+@pytest.mark.parametrize("where", ["key nan", "rope nan", "rope inf", "query nan", "query inf"])
+@pytest.mark.parametrize("q_lens,kv_lens,j", [([90, 5], [90, 5], 40), ([5, 700], [9, 1500], 1000)])
+def test_prefill_of_values_that_are_not_finite(q_lens, kv_lens, j, where):
+    """Rows that see such a score are NaN; rows before the key, other heads and sequences are not."""
+    q, kv, r, scale = _prefill_inputs(q_lens, kv_lens, 3, 64, 9)
+    ref = L.prefill_reference(q, kv, r, q_lens, kv_lens, scale, L.BOTTOM_RIGHT, 0)
+    b = q_lens.index(max(q_lens))
+    q0, k0 = sum(q_lens[:b]), sum(kv_lens[:b])
+    hit = torch.zeros(ref[1].shape, dtype=torch.bool)
+    sees = torch.arange(q_lens[b]) + kv_lens[b] - q_lens[b] >= j
+    if where == "key nan":
+        kv[k0 + j, 1, 7] = NAN
+        hit[q0:q0 + q_lens[b], 1] = sees
+    elif where.startswith("rope"):
+        r[k0 + j, 9] = INF if where == "rope inf" else NAN
+        q[q0:q0 + q_lens[b], :, 128 + 9] = 1.0
+        ref = L.prefill_reference(q, kv, r.nan_to_num(0.0, 0.0), q_lens, kv_lens, scale, L.BOTTOM_RIGHT, 0)
+        hit[q0:q0 + q_lens[b]] = sees[:, None]
+    else:
+        q[q0 + 33, 2, 11] = NAN if where == "query nan" else INF
+        hit[q0 + 33, 2] = True
+    o, l = (t.cpu() for t in B.latent_prefill_attn(q.cuda(), kv.cuda(), r.cuda(), L.offsets(q_lens).cuda(),
+                                                   L.offsets(kv_lens).cuda(), scale=scale))
+    clear()
+    assert bool(o[hit].isnan().all())
+    assert not bool((l[hit].isfinite() | l[hit].isneginf()).any())
+    L.check(o[~hit], l[~hit], (ref[0][~hit], ref[1][~hit], ref[2][~hit], ref[3]), 192, where)
