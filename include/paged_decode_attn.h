@@ -491,10 +491,11 @@ typedef struct {
  *
  * Workspace: paged_latent_decode_workspace_bytes(params) bytes; it holds the
  * partial results of sequences that several CTAs share, and every slot read
- * was written earlier in the same call. NULL: the library-owned buffer of
- * paged_decode_attn, under the same rule for calls that may overlap; a call
- * that is being captured into a graph must pass a workspace of its own
- * (PDA_ERR_WORKSPACE otherwise).
+ * was written earlier in the same call. NULL: a library-owned buffer,
+ * one per device for all calls of this entry point, under the same rules as
+ * that of paged_decode_attn (which is another one); a call that is being
+ * captured into a graph must pass a workspace of its own (PDA_ERR_WORKSPACE
+ * otherwise).
  * A page id or length out of range is never used to form an address; it
  * records PDA_ERR_BAD_PAGE and the affected output is unspecified.
  */

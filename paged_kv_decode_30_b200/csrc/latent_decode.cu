@@ -14,7 +14,7 @@ namespace pda {
 // paged_decode_attn.cu
 int* device_error_word();
 int device_sms();
-pda_status library_workspace(size_t bytes, cudaStream_t stream, void** out);
+pda_status latent_library_workspace(size_t bytes, cudaStream_t stream, void** out);
 
 namespace {
 
@@ -105,7 +105,7 @@ pda_status paged_latent_decode(const void* q, const void* latent_pages, const vo
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   void* ws = p.workspace;
   if (ws == nullptr) {
-    if ((st = library_workspace(pl.total, stream, &ws)) != PDA_OK) return st;
+    if ((st = latent_library_workspace(pl.total, stream, &ws)) != PDA_OK) return st;
   } else if (p.workspace_bytes < pl.total) {
     return PDA_ERR_WORKSPACE;
   }

@@ -35,12 +35,17 @@ constexpr int kMergeCostIters = 2;
 constexpr int kCtaFillIters = 1;
 constexpr int kMaxSplits = 128;
 
+struct LibraryBuffer {
+  void* p = nullptr;
+  size_t bytes = 0;
+};
+
 struct DeviceState {
   bool init = false;
   int num_sms = 0;
   int* err = nullptr;        // device address of g_error_word
-  void* ws = nullptr;        // library-owned workspace (grow-only)
-  size_t ws_bytes = 0;
+  LibraryBuffer ws;         // library-owned workspaces (grow-only): of paged_decode_attn,
+  LibraryBuffer latent_ws;  // of paged_latent_decode
 };
 
 DeviceState g_dev[kMaxDevices];
@@ -66,30 +71,30 @@ pda_status device_state(DeviceState** out) {
   return PDA_OK;
 }
 
-// The library-owned workspace, made at least `bytes` large. Growing is
+// A library-owned workspace, made at least `bytes` large. Growing is
 // stream-ordered: the old buffer is released after the work already queued on
 // `stream`, the new one is ready for the work queued next, and neither step
 // synchronises the device. A call being captured into a CUDA graph cannot
 // grow the buffer (the allocation would belong to the graph).
-pda_status grow_library_workspace(DeviceState* dev, size_t bytes, cudaStream_t stream, void** out) {
+pda_status grow_library_buffer(LibraryBuffer* buf, size_t bytes, cudaStream_t stream, void** out) {
   std::lock_guard<std::mutex> lock(g_mu);
-  if (dev->ws_bytes >= bytes) {
-    *out = dev->ws;
+  if (buf->bytes >= bytes) {
+    *out = buf->p;
     return PDA_OK;
   }
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) return PDA_ERR_CUDA;
   if (cap != cudaStreamCaptureStatusNone) return PDA_ERR_WORKSPACE;
-  if (dev->ws && cudaFreeAsync(dev->ws, stream) != cudaSuccess) return PDA_ERR_CUDA;
-  dev->ws = nullptr;
-  dev->ws_bytes = 0;
+  if (buf->p && cudaFreeAsync(buf->p, stream) != cudaSuccess) return PDA_ERR_CUDA;
+  buf->p = nullptr;
+  buf->bytes = 0;
   void* fresh = nullptr;
   if (cudaMallocAsync(&fresh, bytes, stream) != cudaSuccess) {
     (void)cudaGetLastError();
     return PDA_ERR_WORKSPACE;
   }
-  dev->ws = *out = fresh;
-  dev->ws_bytes = bytes;
+  buf->p = *out = fresh;
+  buf->bytes = bytes;
   return PDA_OK;
 }
 
@@ -267,16 +272,17 @@ int device_sms() {
   return device_state(&st) == PDA_OK ? st->num_sms : 0;
 }
 
-// The library-owned workspace, at least `bytes` large, for a call that is not
-// being captured (PDA_ERR_WORKSPACE otherwise).
-pda_status library_workspace(size_t bytes, cudaStream_t stream, void** out) {
+// The library-owned workspace of paged_latent_decode, at least `bytes` large, for a
+// call that is not being captured (PDA_ERR_WORKSPACE otherwise). It is not the one of
+// paged_decode_attn, which captured calls may hold: growing would take it from them.
+pda_status latent_library_workspace(size_t bytes, cudaStream_t stream, void** out) {
   DeviceState* dev = nullptr;
   pda_status st = device_state(&dev);
   if (st != PDA_OK) return st;
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) return PDA_ERR_CUDA;
   if (cap != cudaStreamCaptureStatusNone) return PDA_ERR_WORKSPACE;
-  return grow_library_workspace(dev, bytes, stream, out);
+  return grow_library_buffer(&dev->latent_ws, bytes, stream, out);
 }
 
 cudaError_t launch_merge(int D, const float* o_parts, const float* lse_parts,
@@ -417,7 +423,7 @@ pda_status paged_decode_attn(const void* q, const void* k_pages, const void* v_p
   if (wl.total > 0) {
     void* ws = p.workspace;
     if (ws == nullptr) {
-      if ((st = grow_library_workspace(dev, wl.total, stream, &ws)) != PDA_OK) return st;
+      if ((st = grow_library_buffer(&dev->ws, wl.total, stream, &ws)) != PDA_OK) return st;
     } else if (p.workspace_bytes < wl.total) {
       return PDA_ERR_WORKSPACE;
     }
