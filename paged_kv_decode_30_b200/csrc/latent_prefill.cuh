@@ -196,6 +196,7 @@ __global__ void __launch_bounds__(PrefillCfg::THREADS, 1)
     __syncthreads();
     b = *mine % a.B;
     tile = a.tiles - 1 - *mine / a.B;
+    fence_proxy_async_smem();  // (Q lands where the costs lay)
     __syncthreads();
   }
   const int qb = __ldg(a.q_offsets + b), nq_all = __ldg(a.q_offsets + b + 1) - qb;
