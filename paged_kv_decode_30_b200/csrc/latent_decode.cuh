@@ -318,9 +318,9 @@ struct LatentCfg {
   static constexpr int OFF_ITEM = OFF_CREDIT + (FP8 ? 2 * NT * 4 : 0);
   static constexpr int ITEMS = 4;
   static constexpr int OFF_BAR = OFF_ITEM + ITEMS * (int)sizeof(LatentItem);
-  static constexpr int BARS = 2 * SLOTS + 2 * R_SLOTS + 2 + 2 + 2 + 3 + 2 * ITEMS;
-  static constexpr int OFF_MISC = OFF_BAR + BARS * 8;   // TMEM address, abort flag, scan sums
-  static constexpr int SMEM = OFF_MISC + 16 + 32 * 4;
+  static constexpr int BARS = 2 * SLOTS + 2 * R_SLOTS + 2 + 2 + 2 + 3 + 2 + 2 * ITEMS;
+  static constexpr int OFF_MISC = OFF_BAR + BARS * 8;   // TMEM address, abort flag, counts of loads, scan sums
+  static constexpr int SMEM = OFF_MISC + 32 + 32 * 4;
   static constexpr int SMEM_ALLOC = SMEM + 1024;
   static constexpr int RH = NT == 64 ? 16 : 8;          // query rows per softmax thread
   static constexpr int GROUPS = NT / RH;
@@ -428,11 +428,13 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
   uint64_t* q_full = o_full + 2;             // Q of the item in shared memory
   uint64_t* q_free = q_full + 1;             // S^T products of the item done
   uint64_t* o_free = q_free + 1;             // O^T of the item read back
-  uint64_t* item_full = o_free + 1;          // [ITEMS]
+  uint64_t* drain = o_free + 1;              // [2] after giving up: an issuer's products done
+  uint64_t* item_full = drain + 2;           // [ITEMS]
   uint64_t* item_free = item_full + C::ITEMS;  // [ITEMS]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
-  int* sums = reinterpret_cast<int*>(smem + C::OFF_MISC + 16);  // [WARPS]
+  int* loads = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);  // units, rotated parts, Qs asked for
+  int* sums = reinterpret_cast<int*>(smem + C::OFF_MISC + 32);  // [WARPS]
   LatentItem* items = reinterpret_cast<LatentItem*>(smem + C::OFF_ITEM);
 
   LatentShares shares;  // (the loads go out first)
@@ -468,7 +470,7 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
   if (warp == 3) {
     // ======================= schedule (whole warp) =============================
     const int i0 = rt * NT / a.H, i1 = (min(a.M, rt * NT + NT) - 1) / a.H;  // query rows of the row tile
-    int j = 0;
+    int j = 0, qloads = 0;
     bool ok = true;
     auto publish = [&](int b, int kv_len, int t0, int t1, bool whole, bool goes_on) {  // uniform over the warp
       if (j >= C::ITEMS)
@@ -483,6 +485,7 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
       mbar_arrive(&item_full[j % C::ITEMS]);
       if (!FP8 && b >= 0) {  // Q rows by TMA, once the item before has been multiplied
         if (j >= 1) ok = __all_sync(FULL, wait_or_abort(q_free, (j - 1) & 1, abort_flag, a.err));
+        qloads += ok;
         if (ok && lane == 0) {
           mbar_arrive_expect_tx(q_full, C::Q_BYTES);
 #pragma unroll 1
@@ -495,6 +498,7 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
     };
     const int2 cut = latent_schedule<C::WARPS>(a, shares, sums, team, lane, ok, publish);
     if (!ok) *abort_flag = 1;
+    if (lane == 0) loads[2] = qloads;
     if (rt == 0 && lane == 0) a.cut[team] = cut;
     __syncwarp();
   } else if (warp == 0) {
@@ -506,7 +510,7 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
       asm volatile("prefetch.tensormap [%0];" ::"l"(&map_r) : "memory");
     }
     const int seg_rows = min(a.page_size, kTile), log2_seg = min(a.log2_page, 7);
-    int g = 0, blk = 0;
+    int g = 0, blk = 0, ropes = 0;
     bool ok = true;
     for (int j = 0; ok; ++j) {
       ok = __all_sync(FULL, wait_or_abort(&item_full[j % C::ITEMS], (j / C::ITEMS) & 1, abort_flag, a.err));
@@ -534,6 +538,7 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
         __syncwarp();
         if (lane < nseg)
           tma_load_2d(sbase + C::OFF_ROPE + rs * C::ROPE_SLOT + lane * seg_rows * 128, &map_r, 0, row, &rfull[rs]);
+        ++ropes;
         return true;
       };
       int pid = page_of(d.first), pid_next = page_of(d.first + 1);
@@ -574,15 +579,10 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
         if (C::OVERLAY && !load_rope(nseg, row)) break;
       }
     }
-    if (!ok) {
-      if (lane == 0) {
-        *abort_flag = 1;
-        // copies already issued land before the CTA's shared memory goes away
-        for (int n = max(0, blk - C::SLOTS); n < blk; ++n)
-          mbar_wait(&full[n % C::SLOTS], (n / C::SLOTS) & 1, a.err, kWaitTimeoutCycles / 16);
-        for (int n = max(0, g - C::R_SLOTS); n < g; ++n)
-          mbar_wait(&rfull[n % C::R_SLOTS], (n / C::R_SLOTS) & 1, a.err, kWaitTimeoutCycles / 16);
-      }
+    if (!ok) *abort_flag = 1;
+    if (lane == 0) {
+      loads[0] = blk;
+      loads[1] = ropes;
     }
     __syncwarp();
   } else if (warp == 1 || warp == 2) {
@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
     // one operand differ by constants in their address field.
     const bool leader = elect_one();
     bool ok = true;
-    int g = 0, blk = 0, issued = 0;
+    int g = 0, blk = 0;
     auto agreed = [&](bool v) { return __all_sync(FULL, v); };
     for (int j = 0; ok; ++j) {
       ok = agreed(wait_or_abort(&item_full[j % C::ITEMS], (j / C::ITEMS) & 1, abort_flag, a.err));
@@ -653,7 +653,6 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
           if (C::OVERLAY && !rope_product()) break;
           if (leader) umma_commit(&s_full[bb]);
           __syncwarp();
-          issued = g + 1;
         }
         if (ok && leader) umma_commit(q_free);
       } else {
@@ -692,15 +691,10 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
             umma_commit(&o_full[bb]);
           }
           __syncwarp();
-          issued = g + 1;
         }
       }
     }
     if (!ok) *abort_flag = 1;
-    if (*abort_flag && issued > 0) {  // MMAs already issued finish before TMEM is freed
-      uint64_t* last = warp == 1 ? &s_full[(issued - 1) & 1] : &o_full[(issued - 1) & 1];
-      mbar_wait(last, ((issued - 1) >> 1) & 1, a.err, kWaitTimeoutCycles / 16);
-    }
     __syncwarp();
   } else {
     // ======================= softmax ===========================================
@@ -1100,6 +1094,23 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
 
   tmem_fence_before();
   __syncthreads();
+  if (*abort_flag) {  // some role gave up: what was issued finishes before its memory goes away
+    constexpr long long lim = kWaitTimeoutCycles / 16;
+    if (warp == 0 && lane == 0) {  // copies: the last ones into each slot
+      for (int n = max(0, loads[0] - C::SLOTS); n < loads[0]; ++n)
+        mbar_wait(&full[n % C::SLOTS], (n / C::SLOTS) & 1, a.err, lim);
+      for (int n = max(0, loads[1] - C::R_SLOTS); n < loads[1]; ++n)
+        mbar_wait(&rfull[n % C::R_SLOTS], (n / C::R_SLOTS) & 1, a.err, lim);
+      if (!FP8 && loads[2] > 0) mbar_wait(q_full, (loads[2] - 1) & 1, a.err, lim);
+    } else if (warp == 1 || warp == 2) {  // products: by the lane that issued them
+      if (elect_one()) {
+        umma_commit(&drain[warp - 1]);
+        mbar_wait(&drain[warp - 1], 0, a.err, lim);
+      }
+      __syncwarp();
+    }
+    __syncthreads();
+  }
   if (warp == 1) {
     tmem_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS)

@@ -50,8 +50,8 @@ struct PrefillCfg {
   static constexpr int OFF_K = OFF_Q + 6 * CHUNK;    // 2 stages x 3 chunks
   static constexpr int OFF_V = OFF_K + 6 * CHUNK;    // 2 chunks
   static constexpr int OFF_BAR = OFF_V + 2 * CHUNK;
-  // q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2][2], o_full[2], turn[2]
-  static constexpr int BARS = 20;
+  // q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2][2], o_full[2], turn[2], drain[2]
+  static constexpr int BARS = 22;
   static constexpr int OFF_MISC = OFF_BAR + BARS * 8;
   static constexpr int SMEM_ALLOC = OFF_MISC + 16 + 1024;
   static constexpr int THREADS = 384;
@@ -218,8 +218,10 @@ __global__ void __launch_bounds__(PrefillCfg::THREADS, 1)
   uint64_t* p_full = s_full + 2;   // [tile][half] weights of 64 keys in TMEM
   uint64_t* o_full = p_full + 4;   // [tile] all products done
   uint64_t* turn = o_full + 2;     // [tile] its products of a step may be issued
+  uint64_t* drain = turn + 2;      // [tile] after giving up: all its products done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  int* loads = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);  // K tiles, V halves asked for
 
   // Key tiles [t0, t1) of either query tile, and keys [lo, hi) that any row sees.
   int t0[2], t1[2], lo_u = 0, hi_u = 0;
@@ -294,9 +296,10 @@ __global__ void __launch_bounds__(PrefillCfg::THREADS, 1)
         if (has_a) load_q(0);
         if (te > tb) load_k(tb);
         if (has_b) load_q(1);
-        int vloads = 0;
+        int kloads = te > tb, vloads = 0;
         for (int t = tb; ok && t < te; ++t) {
           if (t + 1 < te) load_k(t + 1);
+          if (ok && t + 1 < te) ++kloads;
           for (int half = 0; ok && half < 2; ++half) {
             const int n = t - tb;
             if (n >= 1) ok = wait_or_abort(&v_empty[half], (n - 1) & 1, abort_flag, a.err);
@@ -305,20 +308,12 @@ __global__ void __launch_bounds__(PrefillCfg::THREADS, 1)
             mbar_arrive_expect_tx(&v_full[half], C::CHUNK);
             tma_load_3d(dst, &map_kv, C::D, h, kb + t * C::KT + half * 64, &v_full[half]);
             tma_load_3d(dst + C::CHUNK, &map_kv, C::D + 64, h, kb + t * C::KT + half * 64, &v_full[half]);
-          }
-          vloads = t - tb + 1;
-        }
-        if (!ok) {  // copies already issued land before the CTA's shared memory goes away
-          *abort_flag = 1;
-          const long long lim = kWaitTimeoutCycles / 16;
-          if (has_a) mbar_wait(&q_full[0], 0, a.err, lim);
-          if (has_b) mbar_wait(&q_full[1], 0, a.err, lim);
-          for (int n = max(0, vloads - 1); n < vloads + 1; ++n) {
-            mbar_wait(&k_full[n & 1], (n >> 1) & 1, a.err, lim);
-            mbar_wait(&v_full[0], n & 1, a.err, lim);
-            mbar_wait(&v_full[1], n & 1, a.err, lim);
+            ++vloads;
           }
         }
+        if (!ok) *abort_flag = 1;
+        loads[0] = kloads;
+        loads[1] = vloads;
       }
       __syncwarp();
     } else if (warp < 3) {
@@ -330,7 +325,6 @@ __global__ void __launch_bounds__(PrefillCfg::THREADS, 1)
       const int x = warp - 1;
       const bool leader = elect_one();
       bool ok = true;
-      int issued = 0;  // S products so far
       auto agreed = [&](bool v) { return __all_sync(FULL, v); };
       auto scores = [&](int t) {  // S_x = Q_x K(t)^T, K(t) has landed
         const int st = (t - tb) & 1;
@@ -357,7 +351,6 @@ __global__ void __launch_bounds__(PrefillCfg::THREADS, 1)
           umma_commit(&k_empty[st]);
         }
         __syncwarp();
-        ++issued;
       };
       auto key_tile = [&](int t) {
         return agreed(wait_or_abort(&k_full[(t - tb) & 1], ((t - tb) >> 1) & 1, abort_flag, a.err));
@@ -426,8 +419,6 @@ __global__ void __launch_bounds__(PrefillCfg::THREADS, 1)
         __syncwarp();
       }
       if (!ok) *abort_flag = 1;
-      if (*abort_flag && issued > 0)  // MMAs already issued finish before TMEM is freed
-        mbar_wait(&s_full[x], (issued - 1) & 1, a.err, kWaitTimeoutCycles / 16);
       __syncwarp();
     }
   } else {
@@ -536,6 +527,22 @@ __global__ void __launch_bounds__(PrefillCfg::THREADS, 1)
   }
   tmem_fence_before();
   __syncthreads();
+  if (*abort_flag) {  // some role gave up: what was issued finishes before its memory goes away
+    constexpr long long lim = kWaitTimeoutCycles / 16;
+    if (warp == 0 && lane == 0) {  // copies: the last of each kind into each place
+      if (has_a) mbar_wait(&q_full[0], 0, a.err, lim);
+      if (has_b) mbar_wait(&q_full[1], 0, a.err, lim);
+      for (int n = max(0, loads[0] - 2); n < loads[0]; ++n) mbar_wait(&k_full[n & 1], (n >> 1) & 1, a.err, lim);
+      for (int n = max(0, loads[1] - 2); n < loads[1]; ++n) mbar_wait(&v_full[n & 1], (n >> 1) & 1, a.err, lim);
+    } else if (warp == 1 || warp == 2) {  // products: by the lane that issued them
+      if (elect_one()) {
+        umma_commit(&drain[warp - 1]);
+        mbar_wait(&drain[warp - 1], 0, a.err, lim);
+      }
+      __syncwarp();
+    }
+    __syncthreads();
+  }
   if (warp == 1) {
     tmem_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
