@@ -52,7 +52,14 @@ extern "C" pda_status latent_prefill_attn(const void* q, const void* kv, const v
     return PDA_ERR_MISALIGNED;
   const int rows = p.max_q_len < p.total_q ? p.max_q_len : p.total_q;
   const long long tiles = (rows + 2ll * PrefillCfg::QT - 1) / (2 * PrefillCfg::QT);
-  if (tiles * p.batch * p.num_heads > INT_MAX) return PDA_ERR_UNSUPPORTED;
+  // Units of 256 query rows: `tiles` a sequence, or as many as the rows can need, where
+  // that is fewer by a fourth (finding a unit's sequence takes a search then). Rows of
+  // 30 sequences of up to 3000, 16 heads: 696 -> 564 us; 400 of up to 300, a fifth fewer:
+  // 540 -> 555 us; 64 of 500 without a bound on their rows: 985 -> 284 us.
+  const long long by_tiles = tiles * p.batch, by_rows = p.total_q / 256ll + p.batch;
+  const bool rows_fit = 4 * by_rows <= 3 * by_tiles;
+  const long long units = rows_fit ? by_rows : by_tiles;
+  if (units * p.num_heads > INT_MAX) return PDA_ERR_UNSUPPORTED;
   PrefillArgs a{};
   a.q_offsets = q_offsets;
   a.kv_offsets = kv_offsets;
@@ -66,6 +73,8 @@ extern "C" pda_status latent_prefill_attn(const void* q, const void* kv, const v
   a.total_kv = p.total_kv;
   a.max_q = rows;
   a.tiles = (int)tiles;
+  a.units = (int)units;
+  a.by_rows = rows_fit;
   a.causal_offset = p.causal_offset;
   a.window = p.window;
   a.scale_log2 = p.scale * 1.4426950408889634f;
@@ -87,7 +96,7 @@ extern "C" pda_status latent_prefill_attn(const void* q, const void* kv, const v
       return PDA_ERR_CUDA;
     __atomic_fetch_or(&attr_set, bit, __ATOMIC_RELEASE);
   }
-  latent_prefill_kernel<<<dim3((unsigned)(tiles * p.batch * p.num_heads)), PrefillCfg::THREADS,
+  latent_prefill_kernel<<<dim3((unsigned)(units * p.num_heads)), PrefillCfg::THREADS,
                           PrefillCfg::SMEM_ALLOC, reinterpret_cast<cudaStream_t>(stream)>>>(mq, mkv, mr, a);
   return cudaGetLastError() == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
 }

@@ -39,7 +39,8 @@ struct PrefillArgs {
   uint16_t* out;  // bf16 [total_q, H, 128]
   float* lse;     // [total_q, H] or null
   int* err;
-  int B, H, total_q, total_kv, max_q, tiles, causal_offset, window;
+  int B, H, total_q, total_kv, max_q, tiles, units, causal_offset, window;
+  bool by_rows;  // how units are numbered
   float scale_log2;
 };
 
@@ -68,6 +69,45 @@ __device__ __forceinline__ void prefill_visible(const PrefillArgs& a, int nq, in
   const long long l = a.window > 0 ? pos - a.window + 1 : 0;
   hi = (int)(h < 0 ? 0 : (h > nk ? nk : h));
   lo = (int)(l < 0 ? 0 : (l > nk ? nk : l));
+}
+
+// Units of the grid are 256 query rows of a sequence. Either every sequence has `tiles`
+// units, the last tiles first; or (by_rows) sequence b has the units from q_offsets[b] /
+// 256 + b on, the last units first: that leaves it enough for its rows wherever they
+// begin, and all of them fit total_q / 256 + B however the rows are shared out.
+__device__ __forceinline__ int prefill_begin(const PrefillArgs& a, int b) { return (__ldg(a.q_offsets + b) >> 8) + b; }
+
+// Sequence (-1: none) and tile of unit u, for a whole warp.
+__device__ __forceinline__ void prefill_unit(const PrefillArgs& a, int u, int lane, int& b, int& tile) {
+  if (!a.by_rows) {
+    b = u % a.B;
+    tile = a.tiles - 1 - u / a.B;
+    return;
+  }
+  // the sequences that begin at u or before: 32 at a time, closer and closer
+  u = a.units - 1 - u;
+  int base = 0, span = a.B;
+  for (;;) {
+    const int step = (span + 31) / 32, at = base + lane * step;
+    const int k = __popc(__ballot_sync(0xFFFFFFFFu, lane * step < span && prefill_begin(a, min(at, a.B - 1)) <= u));
+    b = base + (k - 1) * step;
+    if (step == 1 || k == 0) break;
+    base = b;
+    span = min(step, a.B - base);
+  }
+  tile = b >= 0 ? u - prefill_begin(a, b) : 0;
+}
+
+// Whether a sequence's rows and keys lie within the tensors.
+__device__ __forceinline__ bool prefill_fits(const PrefillArgs& a, int qb, int nq, int kb, int nk) {
+  return qb >= 0 && nq >= 0 && nq <= a.total_q - qb && kb >= 0 && nk >= 0 && nk <= a.total_kv - kb;
+}
+
+// Records offsets of sequence b that do not fit (units found by rows may pass it over).
+__device__ __forceinline__ void prefill_check(const PrefillArgs& a, int b) {
+  const int qb = __ldg(a.q_offsets + b), kb = __ldg(a.kv_offsets + b);
+  if (!prefill_fits(a, qb, __ldg(a.q_offsets + b + 1) - qb, kb, __ldg(a.kv_offsets + b + 1) - kb))
+    record_error_at(a.err, kErrBadPage);
 }
 
 // D += A B with A (bf16, K-major) in TMEM.
@@ -163,18 +203,45 @@ __global__ void __launch_bounds__(PrefillCfg::THREADS, 1)
   // The CTAs start in the order of their index; the longest work comes first,
   // so that the SMs finish close together. One sequence's tiles are in that
   // order from the last one down (a causal mask gives it the most keys). Of
-  // several sequences every CTA ranks all (sequence, tile) pairs by their key
-  // tiles, a pair a thread; more pairs than threads keep the order of their tiles.
-  const int h = blockIdx.x % a.H, y = blockIdx.x / a.H, pairs = a.B * a.tiles;
-  int b = y % a.B, tile = a.tiles - 1 - y / a.B;
-  if (a.B > 1 && pairs <= C::THREADS) {
+  // several sequences every CTA ranks all units, (sequence, tile) pairs, by their
+  // key tiles, a unit a thread; more units than threads keep their order.
+  const int h = blockIdx.x % a.H, y = blockIdx.x / a.H;
+  if (a.by_rows && h == 0 && tid == 0 && y < a.B) prefill_check(a, y);
+  int b, tile;
+  if (a.B > 1 && a.units <= C::THREADS) {  // (so there are no more sequences than threads)
     int* cost = reinterpret_cast<int*>(smem);
-    int* mine = cost + C::THREADS;
-    const int pb = tid % a.B, pt = a.tiles - 1 - tid / a.B;
-    int c = -1;  // behind the last pair
-    if (tid < pairs) {
-      const int nq = __ldg(a.q_offsets + pb + 1) - __ldg(a.q_offsets + pb);
-      const int nk = __ldg(a.kv_offsets + pb + 1) - __ldg(a.kv_offsets + pb);
+    int* mine = cost + C::THREADS;  // sequence, tile
+    int pb = -1, pt = 0, nq = 0, nk = 0, c = -1;  // (-1: behind the last unit, or of no sequence)
+    if (!a.by_rows) {
+      if (tid < a.units) {
+        pb = tid % a.B;
+        pt = a.tiles - 1 - tid / a.B;
+        nq = __ldg(a.q_offsets + pb + 1) - __ldg(a.q_offsets + pb);
+        nk = __ldg(a.kv_offsets + pb + 1) - __ldg(a.kv_offsets + pb);
+      }
+    } else {
+      int3* seq = reinterpret_cast<int3*>(mine + 4);  // first unit, rows, keys
+      if (tid < a.B)
+        seq[tid] = make_int3(prefill_begin(a, tid), __ldg(a.q_offsets + tid + 1) - __ldg(a.q_offsets + tid),
+                             __ldg(a.kv_offsets + tid + 1) - __ldg(a.kv_offsets + tid));
+      __syncthreads();
+      if (tid < a.units) {
+        const int u = a.units - 1 - tid;
+        int x = 0, e = a.B;
+        while (x < e) {
+          const int mid = (x + e) >> 1;
+          if (seq[mid].x <= u) x = mid + 1;
+          else e = mid;
+        }
+        pb = x - 1;
+        if (pb >= 0) {
+          pt = u - seq[pb].x;
+          nq = seq[pb].y;
+          nk = seq[pb].z;
+        }
+      }
+    }
+    if (pb >= 0) {
       const int first = pt * 2 * C::QT, last = min(min(nq, a.max_q), first + 2 * C::QT) - 1;
       c = 0;
       if (last >= first) {
@@ -187,21 +254,27 @@ __global__ void __launch_bounds__(PrefillCfg::THREADS, 1)
     cost[tid] = c;
     __syncthreads();
     int rank = 0;
-    for (int k = 0; k < pairs; k += 4) {  // (entries behind the last pair are -1)
+    for (int k = 0; k < a.units; k += 4) {  // (entries behind the last unit are -1)
       const int4 o = *reinterpret_cast<const int4*>(cost + k);
       rank += (o.x > c || (o.x == c && k < tid)) + (o.y > c || (o.y == c && k + 1 < tid)) +
               (o.z > c || (o.z == c && k + 2 < tid)) + (o.w > c || (o.w == c && k + 3 < tid));
     }
-    if (tid < pairs && rank == y) *mine = tid;
+    if (tid < a.units && rank == y) {
+      mine[0] = pb;
+      mine[1] = pt;
+    }
     __syncthreads();
-    b = *mine % a.B;
-    tile = a.tiles - 1 - *mine / a.B;
+    b = mine[0];
+    tile = mine[1];
     fence_proxy_async_smem();  // (Q lands where the costs lay)
     __syncthreads();
+  } else {
+    prefill_unit(a, y, lane, b, tile);
   }
+  if (b < 0) return;
   const int qb = __ldg(a.q_offsets + b), nq_all = __ldg(a.q_offsets + b + 1) - qb;
   const int kb = __ldg(a.kv_offsets + b), nk = __ldg(a.kv_offsets + b + 1) - kb;
-  if (qb < 0 || nq_all < 0 || nq_all > a.total_q - qb || kb < 0 || nk < 0 || nk > a.total_kv - kb) {
+  if (!prefill_fits(a, qb, nq_all, kb, nk)) {
     if (threadIdx.x == 0) record_error_at(a.err, kErrBadPage);
     return;
   }
