@@ -10,9 +10,8 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 from typing import Optional
-
-import torch
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libpaged_decode_attn.so")
@@ -162,6 +161,14 @@ class PdaLatentPrefillParams(ctypes.Structure):
 
 
 _lib = None
+# What works without tensors (load, planning, sizes) works without torch. The latent
+# calls, in which an import statement shows, use this name, set by the first of them.
+torch = sys.modules.get("torch")
+
+
+def _with_torch():
+    global torch
+    import torch
 
 
 def load(path: Optional[str] = None):
@@ -474,6 +481,8 @@ def _on(stream, call, *args, **kw):
     """`call` with `stream` as the current stream, so that what it allocates is ordered
     on that stream (a block that the caller's stream gave back may still be in use
     there). The allocator learns that both streams use the results."""
+    if torch is None:
+        _with_torch()
     caller = torch.cuda.current_stream(args[0].device)
     with torch.cuda.stream(stream):
         res = call(*args, **kw)
@@ -493,6 +502,8 @@ def _row_stride(t):
 def _latent_pools(latent_pages, rope_pages, latent_scales, page_table):
     """Check the pools of a latent cache and its page table. Returns their device,
     (num_pages, page_size, latent_dim), rope_dim, (batch, max_pages) and KV dtype."""
+    if torch is None:
+        _with_torch()
     dev = latent_pages.device
     pools = _sizes("latent_pages", latent_pages, 3)
     num_pages, page, _ = pools
@@ -659,6 +670,8 @@ def latent_prefill_attn(q, kv, k_rope, q_offsets, kv_offsets, *, scale,
         return _on(stream, latent_prefill_attn, q, kv, k_rope, q_offsets, kv_offsets, scale=scale,
                    causal_offset=causal_offset, window=window, max_q_len=max_q_len, out=out,
                    lse=lse, with_lse=with_lse)
+    if torch is None:
+        _with_torch()
     lib = load()
     dev = q.device
     total_q, H, width = _sizes("q", q, 3)
