@@ -565,7 +565,7 @@ def paged_latent_append(latent, rope, row_offsets, page_table, kv_lens, latent_p
     p = _latent_rows(latent, rope, row_offsets, page_table, kv_lens, latent_pages, rope_pages,
                      latent_scales)
     st = load().paged_latent_append(latent.data_ptr(), rope.data_ptr(), row_offsets.data_ptr(),
-                                    page_table.data_ptr(), kv_lens.data_ptr(), p,
+                                    page_table.data_ptr(), _ptr(kv_lens), p,
                                     latent_pages.data_ptr(), rope_pages.data_ptr(),
                                     _current_stream(latent.device, stream))
     if st != 0:
