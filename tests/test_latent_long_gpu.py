@@ -170,3 +170,81 @@ def test_fp8_decode_keeps_long_tails(case, R, Dr, heads, uneven):
     o, l = decode(q, ch, batch_of(heads, True, 100), 1.0)
     ref = definition(q[0], ch, 1.0, torch.full((heads,), n - 1, device="cuda"))
     check(o, l, ref, n, R + Dr, f"{name}, {R}, {heads} heads")
+
+
+# ---------------------------------------------------------------------------
+# whole sequences of many tiles a CTA, in every variant of the kernel
+
+VARIANTS = [  # FP8, latent_dim, rope_dim, heads: 16, 32, 64 (bf16) packed rows a CTA, one or two CTAs a team
+    (False, 512, 64, 16), (False, 512, 64, 20), (False, 512, 32, 64), (False, 512, 64, 128),
+    (False, 256, 64, 5), (False, 256, 32, 32), (False, 256, 64, 40),
+    (True, 512, 64, 16), (True, 512, 64, 20), (True, 512, 32, 64),
+    (True, 256, 64, 5), (True, 256, 32, 32), (True, 256, 64, 40),
+]
+
+
+@pytest.mark.parametrize("n", [2049, 6000, 20001])
+@pytest.mark.parametrize("fp8,R,Dr,heads", VARIANTS)
+def test_decode_walks_long_sequences(fp8, R, Dr, heads, n):
+    ch = cache(n, R, Dr, fp8, n, uneven=True)
+    g = torch.Generator(device="cuda").manual_seed(heads)
+    q = torch.randn((1, heads, R + Dr), generator=g, device="cuda").to(torch.bfloat16)
+    scale = (128 + Dr) ** -0.5 / 2
+    o, l = decode(q, ch, batch_of(heads, fp8, 400), scale)
+    ref = definition(q[0], ch, scale, torch.full((heads,), n - 1, device="cuda"))
+    check(o, l, ref, n, R + Dr, f"{n}, {R}, {heads} heads")
+
+
+def levels(n, seed):
+    """Every tile at a level of its own, between 25 below and 5 above, more or less flat."""
+    g = torch.Generator().manual_seed(seed)
+    tiles = (n + 127) // 128
+    at = torch.rand((tiles, 1), generator=g) * 30 - 25
+    return (at + torch.rand((tiles, 1), generator=g) * 2 * torch.randn((tiles, 128), generator=g)).flatten()[:n]
+
+
+@pytest.mark.parametrize("kind", ["rising", "falling", "waves", "flat", "levels 1", "levels 2", "levels 3"])
+@pytest.mark.parametrize("fp8,R,Dr,heads", VARIANTS)
+def test_decode_moves_its_reference_in_long_sequences(fp8, R, Dr, heads, kind):
+    """Rising: by 8 a tile, so that the accumulators move in every tile."""
+    n = 12000
+    j = torch.arange(n).float()
+    scores = {"rising": j / 16, "falling": -j / 16, "flat": torch.zeros(n),
+              "waves": 30 * torch.sin(j / 500) + j / 1000}.get(kind)
+    if scores is None:
+        scores = levels(n, int(kind.split()[1]))
+    ch = cache(n, R, Dr, fp8, 77, scores, uneven=True)
+    q = torch.zeros((1, heads, R + Dr), dtype=torch.bfloat16, device="cuda")
+    q[0, :, R] = 1 - torch.arange(heads, device="cuda") / (2.0 * heads)
+    o, l = decode(q, ch, batch_of(heads, fp8, 400), 1.0)
+    ref = definition(q[0], ch, 1.0, torch.full((heads,), n - 1, device="cuda"))
+    check(o, l, ref, n, 2, f"{kind}, {R}, {heads} heads")   # (a score is one product, and scaled)
+
+
+@pytest.mark.parametrize("window", [0, 1500])
+@pytest.mark.parametrize("fp8,R,Dr,heads", VARIANTS)
+def test_decode_walks_long_sequences_of_many_lengths(fp8, R, Dr, heads, window):
+    """Verify rows, and beginnings of one sequence: items of many sizes follow one another in a CTA."""
+    n, q_len = 9000, 3
+    ch = cache(n, R, Dr, fp8, 31, uneven=True)
+    g = torch.Generator(device="cuda").manual_seed(heads)
+    q = torch.randn((q_len, heads, R + Dr), generator=g, device="cuda").to(torch.bfloat16)
+    scale = (128 + Dr) ** -0.5 / 2
+    sizes = [9000, 2, 4097, 0, 130, 8999, 6400, 1]
+    batch = batch_of(q_len * heads, fp8, 400) // 8 * 8
+    lens = torch.tensor(sizes * (batch // 8), dtype=torch.int32)[torch.randperm(batch, generator=torch.Generator().manual_seed(2))]
+    o, l = B.paged_latent_decode(q.expand(batch, *q.shape).contiguous(), ch["latent"], ch["rope"],
+                                 ch["table"].expand(batch, -1).contiguous(), lens.cuda(), scale=scale,
+                                 causal_offset=L.BOTTOM_RIGHT, window=window, latent_scales=ch["scales"])
+    clear()
+    for size in sizes:
+        rows = (lens == size).cuda()
+        keep = [i for i in range(q_len) if size - q_len + i >= 0]   # rows that see a key
+        none = [i for i in range(q_len) if i not in keep]
+        assert not bool(o[rows][:, none].any()) and bool(l[rows][:, none].isneginf().all())
+        if keep:
+            part = dict(ch, n=size, **{k: ch[k][:size] for k in ("c", "r", "exps") if ch[k] is not None})
+            pos = torch.tensor([size - q_len + i for i in keep], device="cuda").repeat_interleave(heads)
+            ref = definition(q[keep].flatten(0, 1), part, scale, pos, window)
+            check(o[rows][:, keep].flatten(1, 2), l[rows][:, keep].flatten(1, 2), ref, size, R + Dr,
+                  f"{size} of many, {R}, {heads} heads")
