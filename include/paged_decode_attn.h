@@ -481,7 +481,7 @@ typedef struct {
  * Accumulation and softmax statistics are fp32; each weight enters the sum
  * over values with 8 significant bits. FP8 caches: the weights are p_j = exp(s_j
  * - lse) times their row's scale 2^e_j, and what is rounded off small ones beyond
- * that adds up to at most 2^-8.9 of the row's sum of p_j 2^e_j, however many
+ * that adds up to at most 2^-9 of the row's sum of p_j 2^e_j, however many
  * there are; a query element enters to 2^-21 of its row's largest, and
  * an infinite one makes its row NaN.
  *

@@ -36,16 +36,17 @@
 // that share a fifth of the probability, the rest on one: all of them became zero,
 // a fifth of the output), so m follows the scores down as well as up. Per row a
 // credit counts how many tiles' worth of such errors, 128 x 2^-14 = 2^-7 each, the
-// weights have paid for: a tile takes one away, and one with a weight of 2, 8, 32 or 128
-// adds 1/2, 2, 8 or 32, a fourth of it. Before it is used up m moves to the tile at hand.
-// What the step rounds off is then at most 2^-7 / 4 = 2^-9 of a row's sum of weights
-// (2^-8.9, as the weights are compared rounded), whatever its length, and a row moves only
-// where its weights stay low. (Normally distributed scores, 2.5 in log2 units, rows of
-// different scales: a group of eight rows moves in 29% of 40 tiles instead of 12% with a
-// running maximum, in 22% of 400 instead of 2%; 2 in log2 units: 5% instead of 2%.)
-// Such scores take 57.3 us instead of 51.6 for two sequences of 110 k tokens, 64 heads,
-// and 61.6 instead of 57.1 for 72 of up to 6000 tokens, 48 rows; with 1/4 replaced by 1/2,
-// 55.3 and 60.4; with HEAD 4 or 6 instead of 5, 63.4 or 57.9 and 68.5 or 62.6.
+// weights have paid for: a tile whose largest weight is w adds w / 4 and takes one away
+// (2^14 w, if all its weights are below the step). Before it is used up m moves to the
+// tile at hand. What the step rounds off is then at most 2^-7 / 4 = 2^-9 of a row's sum
+// of weights, whatever its length, and a row moves only where its weights stay low.
+// (Normally distributed scores, 2.5 in log2 units, rows of different scales: a group of
+// eight rows moves in 20% of 40 tiles instead of 12% with a running maximum, in 11% of
+// 400 instead of 2%; 2 in log2 units: 5% of 40 instead of 2%.) Such scores take 56.8 us
+// instead of 51.9 for two sequences of 110 k tokens, 64 heads, and 61.4 instead of 57.2
+// for 72 of up to 6000 tokens, 48 rows; with w / 2 instead of w / 4, 55.2 and 60.8; with
+// HEAD 4 instead of 5, 58.4 and 62.9; with the largest weights known to a factor of 4
+// only, as bits that take one reduction instead of eight, 57.3 and 61.9.
 //
 // Roles (warps): 0 TMA producer, 1 S^T issuer, 2 O^T issuer, 3 schedule,
 // 4.. softmax (groups of four warps, a thread = a token of S^T = an element of
@@ -297,7 +298,7 @@ struct LatentCfg {
   static constexpr int P_BUFS = (OVERLAY || (NT == 32 && R == 512)) ? 1 : 2;
   static constexpr int R_SLOTS = FP8 && !(NT == 32 && R == 512) ? 2 : 1;
   static constexpr int ROPE_SLOT = HALF;
-  static constexpr int STATE = 20 * NT * 4 + 1024 + (FP8 ? NT * 4 : 0);
+  static constexpr int STATE = 20 * NT * 4 + 1024 + (FP8 ? 8 * NT * 4 : 0);
   static constexpr int FREE = 227 * 1024 - 1024 - STATE - Q_BYTES - (OVERLAY ? 0 : P_BUFS * P_BYTES) -
                               R_SLOTS * ROPE_SLOT;
   static constexpr int SLOTS = FREE / BLK < 3 * UPT ? FREE / BLK : 3 * UPT;
@@ -313,8 +314,8 @@ struct LatentCfg {
   static constexpr int OFF_INV = OFF_LRED + 8 * NT * 4;
   static constexpr int OFF_CS = OFF_INV + NT * 4;       // score scale per row (FP8)
   static constexpr int OFF_RANGE = OFF_CS + NT * 4;     // int2 visible keys per row
-  static constexpr int OFF_LEVEL = OFF_RANGE + NT * 8;  // FP8: [2][4][NT / 8] levels of a tile's weights
-  static constexpr int OFF_CREDIT = OFF_LEVEL + (FP8 ? NT * 4 : 0);    // FP8: [NT] credit, [NT] greatest m
+  static constexpr int OFF_TOP = OFF_RANGE + NT * 8;    // FP8: [2][4][NT] largest weights of a tile
+  static constexpr int OFF_CREDIT = OFF_TOP + (FP8 ? 8 * NT * 4 : 0);  // FP8: [NT] credit, [NT] greatest m
   static constexpr int OFF_ITEM = OFF_CREDIT + (FP8 ? 2 * NT * 4 : 0);
   static constexpr int ITEMS = 4;
   static constexpr int OFF_BAR = OFF_ITEM + ITEMS * (int)sizeof(LatentItem);
@@ -341,10 +342,20 @@ struct LatentCfg {
   // 2^127.
   static constexpr float HEAD = FP8 ? 5.f : 0.f, TOP = FP8 ? 8.75f : 8.f, DOWN = 40.f;
   // What a change of sequence takes, in tiles (queries, sums and stores; bf16 tiles
-  // are twice as long, and go on being loaded meanwhile). Us at 0 / 1 / 2 / 3 / 4 / 6:
-  // bf16, 32 rows, 300 sequences of up to 1500 tokens 69.8 / 65.4 / 67.8 / 70.7 / 72.3
-  // / 76.7; FP8, 16 rows, 200 of up to 4000 70.4 / 64.0 / 60.8 / 56.0 / 57.8 / 58.9; 48
-  // rows, 72 of up to 6000 70.0 / 66.7 / 62.0 / 58.6 / 55.8 / 57.0.
+  // are twice as long, and go on being loaded meanwhile). Us at 0 / 1 / 2 / 3 / 4 / 6 for
+  // 60 to 300 sequences of 0 to 1500 .. 6000 tokens, a head a packed row:
+  //   bf16, R 512, 32 rows 71.7 / 69.7 / 71.9 / 74.3 / 75.8 / 80.2
+  //                64      68.0 / 65.1 / 66.9 / 69.6 / 72.5 / 75.9
+  //                128     65.3 / 59.9 / 60.9 / 61.5 / 61.2 / 61.6
+  //         R 256, 16      63.3 / 62.3 / 62.4 / 63.4 / 64.0 / 65.7
+  //                32      65.7 / 64.6 / 64.6 / 65.5 / 66.7 / 67.9
+  //                64      64.6 / 59.4 / 57.5 / 58.0 / 58.9 / 60.3
+  //   FP8,  R 512, 16      66.8 / 63.4 / 60.4 / 59.3 / 60.3 / 62.7
+  //                32      70.0 / 62.6 / 59.2 / 57.0 / 57.7 / 61.1
+  //                48      73.8 / 70.3 / 65.9 / 62.4 / 62.0 / 65.0
+  //                128     84.4 / 77.9 / 74.1 / 72.6 / 72.4 / 73.9
+  //         R 256, 16      64.7 / 62.2 / 58.5 / 57.4 / 56.2 / 57.2
+  //                32      72.8 / 68.2 / 67.1 / 63.6 / 63.0 / 64.7
   static constexpr int ITEM_COST = !FP8 ? 1 : NT == 16 ? 3 : 4;
 };
 
@@ -361,13 +372,6 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       "[%0], [%1, {%2, %2, %3, %4}], [%5];" ::"r"(dst),
       "l"(map), "r"(0), "r"(col), "r"(group), "r"(smem_addr(bar))
       : "memory");
-}
-
-// Four e4m3 values >= 0 in a word: bits 6, 5, 4, 3 of each byte say whether its value
-// is at least 2, 8, 32, 128 (the exponent field, biased by 7, lies in bits 6 to 3).
-__device__ __forceinline__ uint32_t e4m3_levels(uint32_t v) {
-  const uint32_t l2 = v & 0x40404040u, b5 = v << 1, b4 = v << 2;
-  return l2 | (l2 & (b5 | b4)) >> 1 | (l2 & b5) >> 2 | (l2 & b5 & b4) >> 3;
 }
 
 // 128-byte-swizzled address of 16-byte piece c of row n in a block of rows.
@@ -711,7 +715,7 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
     float* lred = reinterpret_cast<float*>(smem + C::OFF_LRED);
     float* sm_inv = reinterpret_cast<float*>(smem + C::OFF_INV);
     float* sm_cs = reinterpret_cast<float*>(smem + C::OFF_CS);
-    uint32_t* sm_level = reinterpret_cast<uint32_t*>(smem + C::OFF_LEVEL) + grp;
+    float* sm_top = reinterpret_cast<float*>(smem + C::OFF_TOP);
     float* sm_credit = reinterpret_cast<float*>(smem + C::OFF_CREDIT);
     int2* sm_range = reinterpret_cast<int2*>(smem + C::OFF_RANGE);
     const uint32_t s_tm = tmem + lane_off + C::COL_S + (FP8 ? 2 * r0 : r0);
@@ -893,14 +897,12 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
 #pragma unroll
         for (int r = 1; r < RH; ++r) top = fmaxf(top, x[r]);
         const bool moves = named_bar_or(gbar, GT, !good || top > C::TOP || low);
-        // FP8: a row's credit with the tile before, whose levels all warps have left by
-        // then. It is looked at a tile later still, so that two tiles have to be left.
+        // FP8: a row's credit with the tile before, whose largest weights all warps have
+        // left by then. It is looked at a tile later still, so that two tiles have to be left.
         auto credit_of = [&]() {
-          const uint32_t* lv = sm_level + ((g - 1) & 1) * 4 * C::GROUPS;
-          const uint32_t all = lv[0] | lv[C::GROUPS] | lv[2 * C::GROUPS] | lv[3 * C::GROUPS];
-          const int k = __popc((all >> (8 * (i & 3) + (i < 4 ? 4 : 0))) & 15u);
-          const float paid = k > 0 ? 0.5f * (float)(1 << (2 * k - 2)) : 0.f;
-          return sm_credit[r0 + i] + (t > first ? paid - 1.f : 0.f);
+          const float* wt = sm_top + ((g - 1) & 1) * 4 * NT + r0 + i;
+          const float wm = fmaxf(fmaxf(wt[0], wt[NT]), fmaxf(wt[2 * NT], wt[3 * NT]));
+          return sm_credit[r0 + i] + (t > first ? wm * 0.25f - fminf(1.f, wm * 16384.f) : 0.f);
         };
         if (moves) {
           if (!named_bar_and(gbar, GT, good)) {
@@ -1008,9 +1010,12 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
           if constexpr (!FP8)
             f2_unpack(f2_add(bf16x2_to_f2(w[r / 2]), f2_pack(l_rnd[r], l_rnd[r + 1])), l_rnd[r], l_rnd[r + 1]);
         }
-        if constexpr (FP8) {  // which rows have a weight of 2, 8, 32, 128 in this tile
-          const uint32_t lv = __reduce_or_sync(FULL, e4m3_levels(w[0]) << 1 | e4m3_levels(w[1]) >> 3);
-          if (lane == 0) sm_level[((g & 1) * 4 + q4) * C::GROUPS] = lv;
+        if constexpr (FP8) {  // the rows' largest weights of this tile
+#pragma unroll
+          for (int r = 0; r < RH; ++r) {
+            const float wm = redux_max(x[r]);
+            if (lane == r) sm_top[((g & 1) * 4 + q4) * NT + r0 + r] = wm;
+          }
           if (!moves && i < rows) {
             const float credit = credit_of();
             sm_credit[r0 + i] = credit;

@@ -87,7 +87,7 @@ def check(o, l, ref, n, width, what):
     """o [B, rows, R], l [B, rows] of equal sequences. bf16: weights and the result are
     rounded to bf16 and the normaliser adds the rounded weights, 2^-8 (mean |v| + 2 |out|).
     FP8: a weight p 2^e is held to 2^-8 of itself, and what is rounded off beyond that is
-    at most 2^-8.9 of the row's sum of p 2^e, times codes of up to 448; the normaliser is
+    at most 2^-9 of the row's sum of p 2^e, times codes of up to 448; the normaliser is
     unrounded. The scores are off by d_s (width products in fp32, FP8 queries to 2^-21 of
     their row's largest), and a chain of n / 16 products is added up in fp32, each sum
     off by at most 2 U32 of it; the normaliser, n / 128 sums, and a factor of 2^-22 = 4 U32
@@ -98,7 +98,7 @@ def check(o, l, ref, n, width, what):
     d_s = width * L.U32 * big + (2.0 ** -20 * big if weight is not None else 0.0)
     tol = L.U16 * (mean_abs + 2 * out.abs()) + (2 * (d_s + width * L.U32) + n / 8 * L.U32) * (mean_abs + out.abs())
     if weight is not None:
-        tol = tol + 2.0 ** -8.9 * 448 * weight[:, None]
+        tol = tol + 2.0 ** -9 * 448 * weight[:, None]
     worst = float(((o - out).abs() / tol).max())
     off = float(((l - lse).abs() / (d_s + 8 * L.U32 * lse.abs() + n / 128 * 5 * L.U32 + 2.0 ** -20)).max())
     bias = float(((o - out).mean(dim=-1) / out.abs().mean(dim=-1)).abs().max())
