@@ -665,7 +665,7 @@ def latent_prefill_attn(q, kv, k_rope, q_offsets, kv_offsets, *, scale,
     then its values (the up-projection's output); k_rope bf16 [total_kv, Dr],
     shared by the heads; q_offsets, kv_offsets int32 [B + 1]. ``max_q_len``:
     a bound on the query rows of a sequence (default total_q; a tighter one
-    launches fewer idle CTAs). out bf16 [total_q, H, D], lse fp32 [total_q, H]."""
+    launches fewer idle CTAs; rows past it are not computed). out bf16 [total_q, H, D], lse fp32 [total_q, H]."""
     if stream is not None:
         return _on(stream, latent_prefill_attn, q, kv, k_rope, q_offsets, kv_offsets, scale=scale,
                    causal_offset=causal_offset, window=window, max_q_len=max_q_len, out=out,
