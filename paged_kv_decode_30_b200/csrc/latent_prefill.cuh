@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(PrefillCfg::THREADS, 1)
   } else {
     prefill_unit(a, y, lane, b, tile);
   }
-  if (b < 0) return;
+  if (b < 0 || tile < 0) return;  // (offsets that decrease may give a tile in front of their sequence)
   const int qb = __ldg(a.q_offsets + b), nq_all = __ldg(a.q_offsets + b + 1) - qb;
   const int kb = __ldg(a.kv_offsets + b), nk = __ldg(a.kv_offsets + b + 1) - kb;
   if (!prefill_fits(a, qb, nq_all, kb, nk)) {

@@ -87,3 +87,21 @@ def test_prefill_reports_bad_offsets_of_any_sequence(what, count):
         B.latent_prefill_attn(q.cuda(), kv.cuda(), r.cuda(), qo.cuda(), ko.cuda(), scale=scale)
         torch.cuda.synchronize()
         assert B.last_device_error() == BAD_PAGE, (what, at)
+
+
+def test_prefill_with_offsets_that_decrease_writes_no_rows_of_others():
+    """Empty sequences far behind the units that a search of unordered offsets may give them: their
+    rows would lie in front of them. No sequence has rows, so out holds what it held."""
+    count = 640
+    q, kv, r, scale = _prefill_inputs([20000], [20000], 1, 64, 3)
+    qo = torch.full((count + 1,), 20000, dtype=torch.int32)
+    qo[::7] = 1                      # up and down all the way; no sequence has rows
+    qo[1::7] = 1
+    ko = torch.zeros(count + 1, dtype=torch.int32)
+    ko[:-1][(qo[:-1] == 1) & (qo[1:] > 1)] = 5   # those that go up have keys that go down
+    assert not any(qo[b] < qo[b + 1] and ko[b] <= ko[b + 1] for b in range(count))
+    out = torch.full((20000, 1, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    B.latent_prefill_attn(q.cuda(), kv.cuda(), r.cuda(), qo.cuda(), ko.cuda(), scale=scale, out=out)
+    torch.cuda.synchronize()
+    assert B.last_device_error() == BAD_PAGE
+    assert bool((out == 7.0).all())
