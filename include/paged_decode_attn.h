@@ -333,7 +333,11 @@ PDA_API pda_status paged_kv_append(const void* k_new, const void* v_new,
  *                         per kv head (G * q_len; NVFP4 tiles are decoded
  *                         exactly to f16 in shared memory), or FP8 K/V and
  *                         more than 8; any head_dim-128 case with
- *                         PDA_FLAG_TENSOR_CORES;
+ *                         PDA_FLAG_TENSOR_CORES. With FP8 K/V a weight
+ *                         below 2^-14 of its row's largest in a split counts
+ *                         as zero: where very many such keys matter together
+ *                         (long flat tails below a peak), take more splits or
+ *                         PDA_FLAG_CUDA_CORES;
  *   PDA_KERNEL_SPLIT_FMA  CUDA-core kernel (warp-shuffle FMAs, cp.async.bulk
  *                         page copies): everything else, and every case with
  *                         PDA_FLAG_CUDA_CORES.
