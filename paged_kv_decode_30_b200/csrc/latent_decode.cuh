@@ -984,7 +984,7 @@ __global__ void __launch_bounds__(LatentCfg<R, FP8, NT>::THREADS, 1)
           }
         } else {
 #pragma unroll
-          for (int r = 0; r < RH; r += 2) w[r / 2] = pack_bf16x2(x[r], x[r + 1]);
+          for (int r = 0; r < RH; r += 2) w[r / 2] = pack_bf16x2(x[r], x[r + 1]);  // (the type of the other operand)
         }
         // The buffer's last reader: the O^T products P_BUFS tiles ago. (Overlay:
         // the rotated parts of this tile were loaded after those, and read.)
