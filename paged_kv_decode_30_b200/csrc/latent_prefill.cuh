@@ -8,9 +8,10 @@
 //   O += P V    [128, 128 dims]   K: 128 keys, P from TMEM, V from shared memory
 // S (2 x 128 columns) and O (2 x 128) fill TMEM; the weights P, bf16, take the
 // first 64 columns of their S. (bf16 because V is: the operands of a product have one
-// type. A second term for what bf16 leaves of a weight would be half as many products
-// again; without it an output is off by 1.2 to 1.4 times what its own rounding is.) The two tiles run half a step apart: while the
-// softmax warps of one tile work, the tensor core has the other tile's products,
+// type. A second term for what bf16 leaves of a weight would make 28 products of a
+// step's 20; without it an output is 1.2 to 1.4 times as far off as one rounding.) The
+// two tiles run half a step apart: while the softmax warps of one tile work, the
+// tensor core has the other tile's products,
 //   P_A V(t), Q_A K(t + 1), P_B V(t), Q_B K(t + 1), ...
 // The products of a CTA execute in the order in which they are issued, so Q_A
 // K(t + 1) overwrites the weights that P_A V(t) has read.
